@@ -514,6 +514,142 @@ sbl_status sbl_backward_dual_ste_ex(const sbl_layer_desc *desc, const uint16_t *
                                     float *dW, const uint8_t *dw_keep, void *workspace,
                                     size_t workspace_bytes, void *stream);
 
+/* --------------------------------------------------- 8-bit block matrices --
+ * A "b8" matrix [rows, cols] holds 8-bit codes and one power of two 2^e per
+ * block of 128 codes along a row.  It is the operand of the block-scaled
+ * tensor-core product (sbl_b8_gemm) and the form in which a training step
+ * keeps activations for its backward (a checkpoint: 1 byte and 1/128 per
+ * element instead of 2 or 4).  The pages have no counterpart: they keep some
+ * linears un-ternarised and describe no storage of activations; the format,
+ * its operators and their definitions are this library's own.
+ *
+ * Value of element (r, c) = code(r, c) * 2^e(r, c / 128).  Quantisation of a
+ * block (128 elements of a row, fewer at the end of a row; with
+ * SBL_B8_TILES 128 x 128 elements):
+ *   a = max |x|;  e = the smallest integer >= -126 with a <= MAX * 2^e
+ *   (MAX = 448 for e4m3, 57344 for e5m2, 127 for int8; e = 0 when a = 0);
+ *   code = x * 2^-e rounded half to even to the type (one rounding: the
+ *   scaling is exact), so results are defined bit for bit.
+ * A block holding an Inf or a NaN gets scale byte 255 and codes 0: all its
+ * values are NaN, in sbl_b8_dequantize, in every operator that reads the
+ * matrix and in the products (the whole row of D).  This is the one place
+ * where the library defines results for non-finite inputs.
+ *
+ * Layout.  codes: [rows, sbl_b8_row_bytes] uint8, row bytes = cols rounded up
+ * to 16, padding bytes 0 where a matrix is written transposed.  scales: the
+ * byte e + 127 of block b of row r at byte
+ *   4 * ((b / 4) * RP + 128 * (r / 128) + 4 * (r % 32) + (r % 128) / 32) + b % 4,
+ * RP = rows rounded up to 128 (the order in which the tensor core takes the
+ * scales of 128 rows); bytes of padded rows and blocks are 127.
+ * sbl_b8_scale_bytes in total.  Both buffers 16-byte aligned.
+ *
+ * Limits: rows <= 2^30; element-wise operators want cols a multiple of 16 up
+ * to 65536 (as every activation); the products take any cols. */
+typedef enum { SBL_B8_E4M3 = 0, SBL_B8_E5M2 = 1, SBL_B8_I8 = 2 } sbl_b8_type;
+typedef enum { SBL_B8_ROWS = 0, SBL_B8_TILES = 1 } sbl_b8_blocks;
+typedef struct {
+    int32_t rows;
+    int32_t cols;
+    int32_t type; /* sbl_b8_type */
+} sbl_b8_desc;
+typedef struct {
+    uint8_t *codes;
+    uint8_t *scales;
+} sbl_b8;
+
+/* Bytes per row of codes; bytes of scales.  0 for an invalid descriptor. */
+size_t sbl_b8_row_bytes(const sbl_b8_desc *desc);
+size_t sbl_b8_scale_bytes(const sbl_b8_desc *desc);
+
+/* Quantise X [rows, cols] (bf16 bits, or fp32 when x_is_fp32), row stride ldx
+ * elements (rows 16-byte aligned), into `out` (blocks along rows, or 128 x 128
+ * tiles) and / or `out_t`, the transposed matrix [cols, rows] of the same type
+ * (descriptor {cols, rows, type}).  Either may be NULL.  With SBL_B8_TILES the
+ * two hold the same values; with SBL_B8_ROWS out_t is quantised from X in its
+ * own blocks of 128 along rows.  One launch; X is read once. */
+sbl_status sbl_b8_quantize(const sbl_b8_desc *desc, const void *X, int32_t x_is_fp32, int64_t ldx, sbl_b8_blocks blocks,
+                           const sbl_b8 *out, const sbl_b8 *out_t, void *stream);
+
+/* out_t [cols, rows] of type type_t = the values of `in` (desc) transposed and
+ * quantised in blocks along its rows.  One launch. */
+sbl_status sbl_b8_transpose(const sbl_b8_desc *desc, const sbl_b8 *in, int32_t type_t, const sbl_b8 *out_t, void *stream);
+
+/* X [rows, cols] bf16, row stride ldx = the values of `in`, rounded once
+ * (exact unless below bf16's normal range). */
+sbl_status sbl_b8_dequantize(const sbl_b8_desc *desc, const sbl_b8 *in, uint16_t *X, int64_t ldx, void *stream);
+
+/* D[m, n] (+)= sum_k A[m, k] B[n, k] over the values of two b8 matrices of
+ * e4m3 or e5m2 (mixed allowed; int8: SBL_ERR_UNSUPPORTED) with equal cols;
+ * products and scales exact, fp32 accumulation on the tensor cores.  D: bf16
+ * (rounded once) or fp32, [A rows, B rows], row stride ldd elements (rows
+ * 16-byte aligned); B rows a multiple of 16.  accumulate (fp32 only): D holds
+ * finite values on entry and the product is added to them. */
+sbl_status sbl_b8_gemm(const sbl_b8_desc *a_desc, const sbl_b8 *a, const sbl_b8_desc *b_desc, const sbl_b8 *b, void *D,
+                       int64_t ldd, int32_t d_is_fp32, int32_t accumulate, void *stream);
+
+/* A linear layer on b8 operands, for the linears a model does not ternarise.
+ * W [O, K]: w_desc = {O, K, type}, O and K multiples of 16 up to 65536;
+ * usually quantised with SBL_B8_TILES, whose transposed output is w_t below.
+ * Forward: xq = X [T, K] (bf16, row stride ldx) quantised along rows, an
+ * output that is at once the product's operand and the checkpoint the
+ * backward reads; Y [T, O] = xq w^T (bf16 or fp32, row stride ldy). */
+sbl_status sbl_b8_linear_forward(const sbl_b8_desc *w_desc, const sbl_b8 *w, const uint16_t *X, int64_t ldx, int32_t T,
+                                 int32_t x_type, const sbl_b8 *xq, void *Y, int64_t ldy, int32_t y_is_fp32, void *stream);
+
+/* Its backward from the 8-bit checkpoint:
+ *   dX[T, K] = q(dY) W        dY quantised to g_type along rows (O),
+ *   dW[O, K] (+)= q(dY^T) q(xq^T)^T   both quantised along tokens: dY from
+ *              its bf16 values, xq from the checkpoint's values (type x_type).
+ * w_t: W transposed, descriptor {K, O, type}, for dX; dX may be NULL (w_t
+ * unused), dW may be NULL (xq unused).  dX: [T, K] bf16 or fp32; dW: fp32,
+ * contiguous, added to when dw_accumulate.  T == 0: dX untouched, dW zero
+ * (unless accumulating).  workspace: sbl_b8_linear_workspace_bytes, 256-byte
+ * aligned. */
+size_t sbl_b8_linear_workspace_bytes(const sbl_b8_desc *w_desc, int32_t T);
+sbl_status sbl_b8_linear_backward(const sbl_b8_desc *w_desc, const sbl_b8 *w_t, const sbl_b8 *xq, int32_t x_type,
+                                  const uint16_t *dY, int64_t lddy, int32_t T, int32_t g_type, void *dX, int32_t dx_is_fp32,
+                                  float *dW, int32_t dw_accumulate, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The (gated) activation between an MLP's linears, with 8-bit checkpoints.
+ *   H = act(G) * U (U NULL: H = act(G)); act: silu(g) = g / (1 + e^-g) or
+ *   squared ReLU max(g, 0)^2 (BitNet b1.58 2B4T summary, "Squared ReLU
+ *   Activation in the Feed-Forward Network"); fp32 arithmetic, one rounding.
+ * desc: {T, F, checkpoint type}.  G, U, H: bf16 [T, F] with row strides (rows
+ * 16-byte aligned), so the halves of one [T, 2F] buffer can be passed.  g8,
+ * u8: checkpoints of G and U, each optional, as H is; at least one output.
+ * No output may overlap an input.  One launch. */
+typedef enum { SBL_ACT_SILU = 0, SBL_ACT_RELU2 = 1 } sbl_activation;
+sbl_status sbl_glu_forward(const sbl_b8_desc *desc, sbl_activation act, const uint16_t *G, int64_t ldg, const uint16_t *U,
+                           int64_t ldu, uint16_t *H, int64_t ldh, const sbl_b8 *g8, const sbl_b8 *u8, void *stream);
+
+/* Its gradient at the checkpointed values g, u:
+ *   dG = dH * u * act'(g),  dU = dH * act(g)   (u8 and dU NULL: dG = dH act'(g)).
+ * bf16 with row strides as above; u8 and dU go together. */
+sbl_status sbl_glu_backward(const sbl_b8_desc *desc, sbl_activation act, const sbl_b8 *g8, const sbl_b8 *u8, const uint16_t *dH,
+                            int64_t lddh, uint16_t *dG, int64_t lddg, uint16_t *dU, int64_t lddu, void *stream);
+
+/* sbl_quantize_act_rmsnorm (same Xq, d bit for bit) that also writes the
+ * checkpoint x8 of X; desc: {T, K, checkpoint type}.  eps is a double here (the
+ * statistic is computed in fp64; the other entry point's fp32 eps widened gives
+ * its results).  One launch. */
+sbl_status sbl_quantize_act_rmsnorm_checkpoint(const sbl_b8_desc *desc, const uint16_t *X, const uint16_t *g, double eps,
+                                               int8_t *Xq, float *d, const sbl_b8 *x8, void *stream);
+
+/* Gradient of u = x r g (g NULL: 1), r = 1 / sqrt(mean x^2 + eps), at the
+ * checkpointed x, with respect to x and to g:
+ *   dX[t, k] = r dU g - x r^3 mean_k(dU g x)  (+ dR[t, k], the gradient that
+ *              reaches x past the norm; NULL: none; may be the buffer dX),
+ *   dg[k]    = sum_t dU x r   (NULL: not wanted; needs g).
+ * dU, dR, dX: bf16 [T, K] contiguous; dg: fp32 [K], the same bits for the
+ * same inputs on the same kind of device.  The quantiser's gradient is the
+ * straight-through one of the summary pages (dU = the linear's dX).
+ * workspace (dg only): sbl_rmsnorm_backward_workspace_bytes, 256-byte
+ * aligned.  T == 0: dg zero.  One launch, two with dg. */
+size_t sbl_rmsnorm_backward_workspace_bytes(int32_t T, int32_t K);
+sbl_status sbl_rmsnorm_backward(const sbl_b8_desc *desc, const sbl_b8 *x8, const uint16_t *g, double eps, const uint16_t *dU,
+                                const uint16_t *dR, uint16_t *dX, float *dg, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
 /* Device error word of the current device: 0 when every kernel's bounded
  * waits completed; otherwise a bit per kernel family that gave up a wait.
  * Synchronises the device.  `clear` != 0 resets it to 0 afterwards. */

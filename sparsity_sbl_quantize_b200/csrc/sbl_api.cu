@@ -14,6 +14,7 @@
 #include "sbl_act.cuh"
 #include "sbl_decode.cuh"
 #include "sbl_gemv.cuh"
+#include "sbl_host.h"
 #include "sbl_sp24.cuh"
 #include "sbl_gemm.cuh"
 #include "sbl_pack.cuh"
@@ -21,9 +22,6 @@
 namespace sbl {
 
 __device__ uint32_t g_device_error;
-
-constexpr int kMaxDevices = 64;
-constexpr int64_t kMaxDim = 65536;
 
 struct DeviceInfo {
     bool probed = false;
@@ -35,10 +33,6 @@ struct DeviceInfo {
 static std::mutex g_mutex;
 static DeviceInfo g_devices[kMaxDevices];
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 static EncodeTiledFn g_encode = nullptr;
 
 // Probe the current device once: sm_100, SM count, error word address,
@@ -116,6 +110,18 @@ static sbl_status current_device(DeviceInfo **out)
     }
     if (!di.ok) return SBL_ERR_DEVICE;
     *out = &di;
+    return SBL_OK;
+}
+
+sbl_status host_device(HostDevice *out)
+{
+    DeviceInfo *di = nullptr;
+    const sbl_status st = current_device(&di);
+    if (st != SBL_OK) return st;
+    out->index = static_cast<int>(di - g_devices);
+    out->num_sms = di->num_sms;
+    out->err = di->err;
+    out->encode = g_encode;
     return SBL_OK;
 }
 
@@ -856,7 +862,7 @@ sbl_status sbl_quantize_act_rmsnorm(const uint16_t *X, int32_t T, int32_t K, con
         constexpr int rows = R >= 256 ? 1 : 256 / R;                                      \
         cfg.gridDim = dim3(static_cast<unsigned>((T + rows - 1) / rows));                 \
         cfg.blockDim = dim3(R > 256 ? R : 256);                                           \
-        e = cudaLaunchKernelEx(&cfg, act_norm_quant_kernel<R>, X, T, K, g, eps, Xq, d);   \
+        e = cudaLaunchKernelEx(&cfg, act_norm_quant_kernel<R>, X, T, K, g, static_cast<double>(eps), Xq, d, NormCkpt{}); \
         break;                                                                            \
     }
         SBL_NORM_CASE(32)

@@ -1,0 +1,302 @@
+// sbl_b8.cuh -- quantiser, transposer and reader of b8 matrices (the format:
+// sbl_b8_format.cuh) on sm_100a.
+#pragma once
+
+#include "sbl_b8_format.cuh"
+
+namespace sbl {
+
+// ------------------------------------------------------------ row blocks --
+// One warp per (row, 512 columns): lane l of half h holds the eight values at
+// columns 256 i + 128 h + 8 (l % 16), i = 0, 1, so half h of pass i is one
+// block and the warp writes one scale word.  X is read once; memory bound.
+struct B8RowArgs {
+    const void *X;
+    int64_t ldx;        // elements
+    int32_t rows, cols;
+    uint8_t *codes;
+    int64_t ldc;        // bytes, >= cols
+    uint32_t *scales;
+    int64_t rp;         // rows padded to 128
+    int32_t words;      // scale words per row
+};
+
+template <int TYPE, int SRC>
+__global__ void __launch_bounds__(256) b8_quantize_rows_kernel(B8RowArgs a)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, half = lane >> 4;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t row = unit / a.words;
+    const int w = static_cast<int>(unit - row * a.words);
+    if (row >= a.rp) return;
+    if (row >= a.rows) {
+        if (lane == 0) a.scales[b8_word_index(w, a.rp, row)] = kB8PadWord;
+        return;
+    }
+    uint32_t word = 0;
+    const int64_t c0 = static_cast<int64_t>(w) * 512 + 128 * half + 8 * (lane & 15);
+    if constexpr (SRC == kSrcBf16) {
+        uint4 v[2];
+        const uint16_t *x = static_cast<const uint16_t *>(a.X) + row * a.ldx;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            v[i] = c0 + 256 * i < a.cols ? __ldg(reinterpret_cast<const uint4 *>(x + c0 + 256 * i)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(bf16x8_absmax(v[i])) << 16);
+            if (c0 + 256 * i < a.cols)
+                *reinterpret_cast<uint2 *>(a.codes + row * a.ldc + c0 + 256 * i) = b8_encode_bf16x8<TYPE>(v[i], b8_inv_scale(byte));
+            word |= byte << (8 * (2 * i + half));
+        }
+    } else {
+        float4 v[2][2];
+        const float *x = static_cast<const float *>(a.X) + row * a.ldx;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                v[i][h] = c0 + 256 * i < a.cols ? __ldg(reinterpret_cast<const float4 *>(x + c0 + 256 * i) + h)
+                                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                m = max(m, max(max(__float_as_uint(v[i][h].x) & 0x7fffffffu, __float_as_uint(v[i][h].y) & 0x7fffffffu),
+                               max(__float_as_uint(v[i][h].z) & 0x7fffffffu, __float_as_uint(v[i][h].w) & 0x7fffffffu)));
+            }
+            const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(m));
+            const float inv = b8_inv_scale(byte);
+            if (c0 + 256 * i < a.cols) {
+                uint32_t q[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    q[h] = b8_encode4<TYPE>(b8_scaled(v[i][h].x, inv), b8_scaled(v[i][h].y, inv),
+                                            b8_scaled(v[i][h].z, inv), b8_scaled(v[i][h].w, inv));
+                *reinterpret_cast<uint2 *>(a.codes + row * a.ldc + c0 + 256 * i) = make_uint2(q[0], q[1]);
+            }
+            word |= byte << (8 * (2 * i + half));
+        }
+    }
+    word |= __shfl_xor_sync(0xffffffffu, word, 16);
+    if (lane == 0) a.scales[b8_word_index(w, a.rp, row)] = word;
+}
+
+// Codes and scales back to bf16 (one rounding of code 2^e, exact unless the
+// value lies below bf16's normal range).  The layout of the quantiser.
+struct B8ReadArgs {
+    const uint8_t *codes;
+    int64_t ldc;
+    const uint32_t *scales;
+    int64_t rp;
+    int32_t rows, cols, words;
+    uint16_t *X;
+    int64_t ldx;
+};
+
+template <int TYPE>
+__global__ void __launch_bounds__(256) b8_dequantize_kernel(B8ReadArgs a)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, half = lane >> 4;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t row = unit / a.words;
+    const int w = static_cast<int>(unit - row * a.words);
+    if (row >= a.rows) return;
+    const int64_t c0 = static_cast<int64_t>(w) * 512 + 128 * half + 8 * (lane & 15);
+    const uint32_t word = __ldg(a.scales + b8_word_index(w, a.rp, row));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (c0 + 256 * i >= a.cols) continue;
+        const uint2 q = __ldg(reinterpret_cast<const uint2 *>(a.codes + row * a.ldc + c0 + 256 * i));
+        const float s = b8_scale((word >> (8 * (2 * i + half))) & 0xffu);
+        float lo[4], hi[4];
+        b8_decode4<TYPE>(q.x, lo);
+        b8_decode4<TYPE>(q.y, hi);
+        *reinterpret_cast<uint4 *>(a.X + row * a.ldx + c0 + 256 * i) =
+            make_uint4(pack_bf16(__fmul_rn(lo[0], s), __fmul_rn(lo[1], s)), pack_bf16(__fmul_rn(lo[2], s), __fmul_rn(lo[3], s)),
+                       pack_bf16(__fmul_rn(hi[0], s), __fmul_rn(hi[1], s)), pack_bf16(__fmul_rn(hi[2], s), __fmul_rn(hi[3], s)));
+    }
+}
+
+// ------------------------------------------------------ tiles, transposed --
+// One CTA per 128 x 128 tile; thread (rg, cg) holds the 8 x 8 values at rows
+// 8 rg .., columns 8 cg .. in fp32 or packed bf16, so a row block is the 16
+// lanes of a half warp, a column block is 16 threads of one cg, and a
+// thread's column of eight is eight consecutive bytes of the transposed row.
+// Both orders come from one read of X; the transposed bytes pass through a
+// 16 KiB swizzled tile so that both outputs are written 128 bytes at a time.
+//
+// out   the row blocks (codes nullptr: not written)
+// out_t the same matrix transposed, [cols, rows] (codes nullptr: not written)
+// TILES: one scale per 128 x 128 tile for both.  The transpose is then exact;
+// otherwise its blocks run along the rows of X and have scales of their own.
+struct B8TileArgs {
+    const void *X;      // bf16, fp32 or b8 codes
+    int64_t ldx;        // elements (bytes of a b8 row)
+    const uint32_t *xs; // b8 source: its scales
+    int64_t xrp;
+    int32_t rows, cols;
+    uint8_t *codes;
+    int64_t ldc;
+    uint32_t *scales;
+    int64_t rp;
+    uint8_t *codes_t;
+    int64_t ldt;        // round_up(rows, 16)
+    uint32_t *scales_t;
+    int64_t rpt;        // cols padded to 128
+    int32_t tiles_c;    // column tiles; the grid runs over tiles, columns fastest
+};
+
+template <int TYPE, int SRC, int SRC_TYPE, bool TILES>
+__global__ void __launch_bounds__(256) b8_tile_kernel(B8TileArgs a)
+{
+    __shared__ __align__(16) uint8_t tile[128 * 128];
+    __shared__ uint32_t colmax[16][128];
+    __shared__ uint32_t wmax[8];
+    __shared__ uint8_t rbyte[128], cbyte[128];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int rg = tid >> 4, cg = tid & 15;
+    const int tr = static_cast<int>(blockIdx.x) / a.tiles_c;
+    const int r0 = tr * 128, c0 = (static_cast<int>(blockIdx.x) - tr * a.tiles_c) * 128;
+    const int col = c0 + 8 * cg;
+    const bool col_ok = col < a.cols;
+
+    float v[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = r0 + 8 * rg + i;
+        const bool ok = col_ok && row < a.rows;
+        if constexpr (SRC == kSrcBf16) {
+            const uint4 q = ok ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.X) + row * a.ldx + col))
+                               : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][2 * j] = bf16_lo(w[j]), v[i][2 * j + 1] = bf16_hi(w[j]);
+        } else if constexpr (SRC == kSrcF32) {
+            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.X) + row * a.ldx + col);
+            const float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float4 x = ok ? __ldg(p) : z, y = ok ? __ldg(p + 1) : z;
+            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+            v[i][4] = y.x, v[i][5] = y.y, v[i][6] = y.z, v[i][7] = y.w;
+        } else {
+            const uint2 q = ok ? __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.X) + row * a.ldx + col))
+                               : make_uint2(0u, 0u);
+            const int blk = c0 >> 7;
+            const uint32_t byte = ok ? __ldg(reinterpret_cast<const uint8_t *>(a.xs + b8_word_index(blk >> 2, a.xrp, row)) + (blk & 3)) : 127u;
+            const float s = b8_scale(byte);
+            float lo[4], hi[4];
+            b8_decode4<SRC_TYPE>(q.x, lo);
+            b8_decode4<SRC_TYPE>(q.y, hi);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][j] = __fmul_rn(lo[j], s), v[i][4 + j] = __fmul_rn(hi[j], s);
+        }
+    }
+    auto mag = [](float x) { return __float_as_uint(x) & 0x7fffffffu; };
+    uint32_t rmax[8];  // this thread's row maxima, then the blocks'
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, mag(v[i][j]));
+        rmax[i] = m;
+    }
+    if constexpr (TILES) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, rmax[i]);
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) wmax[tid >> 5] = m;
+        __syncthreads();
+        m = wmax[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) m = max(m, wmax[i]);
+        const uint32_t byte = b8_scale_byte<TYPE>(m);
+        if (tid < 128) rbyte[tid] = cbyte[tid] = static_cast<uint8_t>(byte);
+    } else {
+        if (a.codes) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(rmax[i]));
+                if (cg == 0) rbyte[8 * rg + i] = static_cast<uint8_t>(byte);
+            }
+        }
+        if (a.codes_t) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = max(m, mag(v[i][j]));
+                colmax[rg][8 * cg + j] = m;
+            }
+            __syncthreads();
+            if (tid < 128) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) m = max(m, colmax[i][tid]);
+                cbyte[tid] = static_cast<uint8_t>(b8_scale_byte<TYPE>(m));
+            }
+        }
+    }
+    __syncthreads();
+
+    if (a.codes) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = r0 + 8 * rg + i;
+            if (!col_ok || row >= a.rows) continue;
+            const float inv = b8_inv_scale(rbyte[8 * rg + i]);
+            const uint32_t lo = b8_encode4<TYPE>(b8_scaled(v[i][0], inv), b8_scaled(v[i][1], inv), b8_scaled(v[i][2], inv), b8_scaled(v[i][3], inv));
+            const uint32_t hi = b8_encode4<TYPE>(b8_scaled(v[i][4], inv), b8_scaled(v[i][5], inv), b8_scaled(v[i][6], inv), b8_scaled(v[i][7], inv));
+            *reinterpret_cast<uint2 *>(a.codes + row * a.ldc + col) = make_uint2(lo, hi);
+        }
+        // the tile's column of scale bytes (padded rows: 127; a word's blocks
+        // past the last column are filled by the last block's tile)
+        if (tid < 128) {
+            const int64_t row = r0 + tid;
+            const int blk = c0 >> 7, nblk = (a.cols + 127) >> 7;
+            uint8_t *p = reinterpret_cast<uint8_t *>(a.scales + b8_word_index(blk >> 2, a.rp, row));
+            p[blk & 3] = row < a.rows ? rbyte[tid] : 127;
+            if (blk == nblk - 1)
+                for (int b = (blk & 3) + 1; b < 4; ++b) p[b] = 127;
+        }
+    }
+    if (a.codes_t) {
+        // eight bytes (rows 8 rg ..) of transposed row 8 cg + j, the 16-byte
+        // chunk rg / 2 at position (rg / 2) ^ (cg % 8)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float inv = b8_inv_scale(cbyte[8 * cg + j]);
+            const uint32_t lo = b8_encode4<TYPE>(b8_scaled(v[0][j], inv), b8_scaled(v[1][j], inv), b8_scaled(v[2][j], inv), b8_scaled(v[3][j], inv));
+            const uint32_t hi = b8_encode4<TYPE>(b8_scaled(v[4][j], inv), b8_scaled(v[5][j], inv), b8_scaled(v[6][j], inv), b8_scaled(v[7][j], inv));
+            *reinterpret_cast<uint2 *>(tile + (8 * cg + j) * 128 + (((rg >> 1) ^ (cg & 7)) << 4) + 8 * (rg & 1)) = make_uint2(lo, hi);
+        }
+        __syncthreads();
+        // rows past the last are zero codes, so whole 16-byte chunks are
+        // written up to the padded row length
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int k = p * 256 + tid;
+            const int tc = k >> 3, ch = k & 7;
+            const int trow = c0 + tc;
+            if (trow < a.cols && r0 + 16 * ch < a.ldt)
+                *reinterpret_cast<uint4 *>(a.codes_t + trow * a.ldt + r0 + 16 * ch) =
+                    *reinterpret_cast<const uint4 *>(tile + tc * 128 + ((ch ^ ((tc >> 3) & 7)) << 4));
+        }
+        if (tid < 128) {
+            const int64_t trow = c0 + tid;
+            const int blk = r0 >> 7, nblk = (a.rows + 127) >> 7;
+            uint8_t *p = reinterpret_cast<uint8_t *>(a.scales_t + b8_word_index(blk >> 2, a.rpt, trow));
+            p[blk & 3] = trow < a.cols ? cbyte[tid] : 127;
+            if (blk == nblk - 1)
+                for (int b = (blk & 3) + 1; b < 4; ++b) p[b] = 127;
+        }
+    }
+}
+
+}  // namespace sbl

@@ -1,0 +1,372 @@
+// sbl_ckpt.cuh -- the gated activation and the RMSNorm with 8-bit activation
+// checkpoints (the b8 format) on sm_100a.
+//
+// Between two linears a training step keeps what their backward reads: the
+// pre-activations of the MLP and the norms' inputs, 2 bytes an element.  The
+// forward kernels here write them as b8 matrices instead (1 byte and 1/128),
+// from the registers that hold the bf16 inputs anyway, and the backward
+// kernels read only those.  The backward is the exact gradient of the formula
+// at the checkpointed values.
+#pragma once
+
+#include "sbl_b8.cuh"
+
+namespace sbl {
+
+enum ActKind : int { kActSilu = 0, kActRelu2 = 1 };
+
+// act(g), and act'(g) beside it.  relu2(g) = max(g, 0)^2, relu2' = 2 max(g, 0).
+// silu(g) = g s, s = 1 / (1 + e^-g), silu' = s (1 + g (1 - s)), with
+// t = e^-|g| <= 1:  s = (g < 0 ? t : 1) / (1 + t),  1 - s = (g < 0 ? 1 : t) / (1 + t),
+// so that nothing overflows and far negative g keep their (tiny) values.
+// __expf is off by about |g| 2^-23 and __fdividef by 2^-22, far below the
+// bf16 results' half step of 2^-8.
+template <int ACT>
+__device__ __forceinline__ float act_value(float g)
+{
+    if constexpr (ACT == kActRelu2) {
+        const float p = g < 0.0f ? 0.0f : g;  // a NaN stays one
+        return p * p;
+    } else {
+        const float t = __expf(-fabsf(g));
+        return g * __fdividef(g < 0.0f ? t : 1.0f, 1.0f + t);
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_value_grad(float g, float &a, float &da)
+{
+    if constexpr (ACT == kActRelu2) {
+        const float p = g < 0.0f ? 0.0f : g;
+        a = p * p;
+        da = 2.0f * p;
+    } else {
+        const float t = __expf(-fabsf(g));
+        const float inv = __fdividef(1.0f, 1.0f + t);
+        const float s = g < 0.0f ? t * inv : inv, rest = g < 0.0f ? inv : t * inv;
+        a = g * s;
+        da = s * fmaf(g, rest, 1.0f);
+    }
+}
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4 &q, float (&v)[8])
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8])
+{
+    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+
+// h = act(g) u (u absent: h = act(g)), with the checkpoints of g and u.  The
+// layout of the row quantiser: a warp per (row, 512 columns).  Memory bound:
+// per element 4 bytes read, 2 + 2 written.
+struct GluFwdArgs {
+    const uint16_t *G, *U;  // U nullptr: not gated
+    int64_t ldg, ldu;
+    uint16_t *H;            // nullptr: only the checkpoints
+    int64_t ldh;
+    uint8_t *gc, *uc;       // checkpoint codes (nullptr: none)
+    uint32_t *gs, *us;
+    int64_t ldc;
+    int64_t rp;
+    int32_t rows, cols, words;
+};
+
+template <int TYPE, int ACT, bool GATED>
+__global__ void __launch_bounds__(256) glu_forward_kernel(GluFwdArgs a)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, half = lane >> 4;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t row = unit / a.words;
+    const int w = static_cast<int>(unit - row * a.words);
+    if (row >= a.rp) return;
+    const int64_t wi = b8_word_index(w, a.rp, row);
+    if (row >= a.rows) {
+        if (lane == 0) {
+            if (a.gc) a.gs[wi] = kB8PadWord;
+            if (GATED && a.uc) a.us[wi] = kB8PadWord;
+        }
+        return;
+    }
+    const int64_t c0 = static_cast<int64_t>(w) * 512 + 128 * half + 8 * (lane & 15);
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    uint4 g[2], u[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool ok = c0 + 256 * i < a.cols;
+        g[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(a.G + row * a.ldg + c0 + 256 * i)) : z;
+        u[i] = GATED && ok ? __ldg(reinterpret_cast<const uint4 *>(a.U + row * a.ldu + c0 + 256 * i)) : z;
+    }
+    uint32_t gw = 0, uw = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t c = c0 + 256 * i;
+        const bool ok = c < a.cols;
+        if (a.H && ok) {
+            float gv[8], uv[8], h[8];
+            unpack_bf16x8(g[i], gv);
+            unpack_bf16x8(u[i], uv);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h[k] = GATED ? act_value<ACT>(gv[k]) * uv[k] : act_value<ACT>(gv[k]);
+            *reinterpret_cast<uint4 *>(a.H + row * a.ldh + c) = pack_bf16x8(h);
+        }
+        if (a.gc) {
+            const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(bf16x8_absmax(g[i])) << 16);
+            if (ok) *reinterpret_cast<uint2 *>(a.gc + row * a.ldc + c) = b8_encode_bf16x8<TYPE>(g[i], b8_inv_scale(byte));
+            gw |= byte << (8 * (2 * i + half));
+        }
+        if (GATED && a.uc) {
+            const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(bf16x8_absmax(u[i])) << 16);
+            if (ok) *reinterpret_cast<uint2 *>(a.uc + row * a.ldc + c) = b8_encode_bf16x8<TYPE>(u[i], b8_inv_scale(byte));
+            uw |= byte << (8 * (2 * i + half));
+        }
+    }
+    if (a.gc) {
+        gw |= __shfl_xor_sync(0xffffffffu, gw, 16);
+        if (lane == 0) a.gs[wi] = gw;
+    }
+    if (GATED && a.uc) {
+        uw |= __shfl_xor_sync(0xffffffffu, uw, 16);
+        if (lane == 0) a.us[wi] = uw;
+    }
+}
+
+// dg = dh u act'(g), du = dh act(g) at the checkpointed g and u.
+struct GluBwdArgs {
+    const uint8_t *gc, *uc;
+    const uint32_t *gs, *us;
+    int64_t ldc, rp;
+    const uint16_t *dH;
+    int64_t ldh;
+    uint16_t *dG, *dU;
+    int64_t ldg, ldu;
+    int32_t rows, cols, words;
+};
+
+template <int TYPE>
+__device__ __forceinline__ void b8_load8(const uint2 &q, float s, float (&v)[8])
+{
+    float lo[4], hi[4];
+    b8_decode4<TYPE>(q.x, lo);
+    b8_decode4<TYPE>(q.y, hi);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __fmul_rn(lo[k], s), v[4 + k] = __fmul_rn(hi[k], s);
+}
+
+template <int TYPE, int ACT, bool GATED>
+__global__ void __launch_bounds__(256) glu_backward_kernel(GluBwdArgs a)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, half = lane >> 4;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t row = unit / a.words;
+    const int w = static_cast<int>(unit - row * a.words);
+    if (row >= a.rows) return;
+    const int64_t wi = b8_word_index(w, a.rp, row);
+    const uint32_t gw = __ldg(a.gs + wi), uw = GATED ? __ldg(a.us + wi) : 0u;
+    const int64_t c0 = static_cast<int64_t>(w) * 512 + 128 * half + 8 * (lane & 15);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t c = c0 + 256 * i;
+        if (c >= a.cols) continue;
+        const uint2 gq = __ldg(reinterpret_cast<const uint2 *>(a.gc + row * a.ldc + c));
+        const uint2 uq = GATED ? __ldg(reinterpret_cast<const uint2 *>(a.uc + row * a.ldc + c)) : make_uint2(0u, 0u);
+        const uint4 hq = __ldg(reinterpret_cast<const uint4 *>(a.dH + row * a.ldh + c));
+        const int sh = 8 * (2 * i + half);
+        float g[8], u[8], dh[8], dg[8], du[8];
+        b8_load8<TYPE>(gq, b8_scale((gw >> sh) & 0xffu), g);
+        if (GATED) b8_load8<TYPE>(uq, b8_scale((uw >> sh) & 0xffu), u);
+        unpack_bf16x8(hq, dh);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float v, d;
+            act_value_grad<ACT>(g[k], v, d);
+            dg[k] = GATED ? dh[k] * u[k] * d : dh[k] * d;
+            du[k] = dh[k] * v;
+        }
+        *reinterpret_cast<uint4 *>(a.dG + row * a.ldg + c) = pack_bf16x8(dg);
+        if (GATED) *reinterpret_cast<uint4 *>(a.dU + row * a.ldu + c) = pack_bf16x8(du);
+    }
+}
+
+// RMSNorm backward from the checkpointed input.  With v_k = du_k gain_k,
+//   r = (sum x^2 / K + eps)^-1/2,  c = r^3 / K sum_k v_k x_k,
+//   dx_k = r v_k - c x_k (+ residual gradient),   dgain_k = sum_t du x r.
+// RT threads share a row; thread lt holds the 8-element chunks lt + j RT
+// (j < NC), so both sums are one pass over registers and the row is read
+// once.  A CTA takes rows in steps of the grid and keeps its part of dgain in
+// registers; the parts meet in shared memory (rows of one CTA, in order) and
+// then in norm_dgain_kernel (CTAs, in order), so the result is the same every
+// time.
+constexpr int kNormPartials = 512;  // most CTAs that leave a partial dgain
+
+struct NormBwdArgs {
+    const uint8_t *xc;
+    const uint32_t *xs;
+    int64_t ldc, rp;
+    const uint16_t *gain;  // nullptr: 1
+    const uint16_t *dU;
+    const uint16_t *dR;    // nullptr: none
+    uint16_t *dX;
+    float *partial;        // [grid, K]; nullptr: no dgain
+    int32_t T, K;
+    float eps;
+};
+
+template <int TYPE, int RT, int NC>
+__global__ void __launch_bounds__(RT > 256 ? RT : 256) norm_backward_kernel(NormBwdArgs a)
+{
+    constexpr int kRows = RT >= 256 ? 1 : 256 / RT;  // rows of one step
+    constexpr int W = RT / 32;
+    __shared__ float2 red[2][kRows][W];
+    extern __shared__ float dg_sh[];  // [K]
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int sub = threadIdx.x / RT, lt = threadIdx.x % RT;
+    const int chunks = a.K / 8;
+    float acc[NC][8];
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[j][k] = 0.0f;
+    int parity = 0;
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kRows; base < a.T;
+         base += static_cast<int64_t>(gridDim.x) * kRows, parity ^= 1) {
+        const int64_t row = base + sub;
+        const bool active = row < a.T;
+        float x[NC][8];
+        uint4 du[NC];
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            const int ci = lt + j * RT;
+            du[j] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[j][k] = 0.0f;
+            if (active && ci < chunks) {
+                const uint2 q = __ldg(reinterpret_cast<const uint2 *>(a.xc + row * a.ldc) + ci);
+                du[j] = __ldg(reinterpret_cast<const uint4 *>(a.dU + row * a.K) + ci);
+                const int blk = ci >> 4;
+                const uint32_t byte =
+                    __ldg(reinterpret_cast<const uint8_t *>(a.xs + b8_word_index(blk >> 2, a.rp, row)) + (blk & 3));
+                b8_load8<TYPE>(q, b8_scale(byte), x[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            const int ci = lt + j * RT;
+            float v[8], g[8];
+            unpack_bf16x8(du[j], v);
+            if (a.gain && ci < chunks) {
+                unpack_bf16x8(__ldg(reinterpret_cast<const uint4 *>(a.gain) + ci), g);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] *= g[k];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                s1 = fmaf(x[j][k], x[j][k], s1);
+                s2 = fmaf(v[k], x[j][k], s2);
+            }
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            s1 += __shfl_xor_sync(0xffffffffu, s1, off);
+            s2 += __shfl_xor_sync(0xffffffffu, s2, off);
+        }
+        if constexpr (W > 1) {
+            // two buffers in turn: one barrier a step suffices
+            if ((lt & 31) == 0) red[parity][sub][lt >> 5] = make_float2(s1, s2);
+            __syncthreads();
+            s1 = s2 = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float2 p = red[parity][sub][w];
+                s1 += p.x;
+                s2 += p.y;
+            }
+        }
+        const float invk = 1.0f / static_cast<float>(a.K);
+        const float r = rsqrtf(s1 * invk + a.eps);
+        const float c = r * r * r * (s2 * invk);
+        if (!active) continue;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            const int ci = lt + j * RT;
+            if (ci >= chunks) continue;
+            float v[8], g[8], o[8], d[8];
+            unpack_bf16x8(du[j], v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                d[k] = v[k];
+                acc[j][k] = fmaf(v[k] * r, x[j][k], acc[j][k]);
+            }
+            if (a.gain) {
+                unpack_bf16x8(__ldg(reinterpret_cast<const uint4 *>(a.gain) + ci), g);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) d[k] *= g[k];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = r * d[k] - c * x[j][k];
+            if (a.dR) {
+                float e[8];
+                unpack_bf16x8(*(reinterpret_cast<const uint4 *>(a.dR + row * a.K) + ci), e);  // dR may be dX
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] += e[k];
+            }
+            *(reinterpret_cast<uint4 *>(a.dX + row * a.K) + ci) = pack_bf16x8(o);
+        }
+    }
+    if (!a.partial) return;
+    for (int s = 0; s < kRows; ++s) {
+        if (sub == s) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                const int ci = lt + j * RT;
+                if (ci >= chunks) continue;
+                float *p = kRows > 1 ? dg_sh + 8 * ci : nullptr;
+                float *o = a.partial + static_cast<int64_t>(blockIdx.x) * a.K + 8 * ci;
+                if (kRows > 1 && s > 0)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) acc[j][k] += p[k];
+                if (s == kRows - 1) {
+                    reinterpret_cast<float4 *>(o)[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+                    reinterpret_cast<float4 *>(o)[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) p[k] = acc[j][k];
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// dgain[k] = the sum of n partial rows, in 8 interleaved parts joined in order.
+__global__ void __launch_bounds__(256) norm_dgain_kernel(const float *__restrict__ partial, int32_t n, int32_t K,
+                                                         float *__restrict__ dgain)
+{
+    __shared__ float sh[8][32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+    const int k = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (k < K)
+        for (int i = part; i < n; i += 8) s += partial[static_cast<int64_t>(i) * K + k];
+    sh[part][lane] = s;
+    __syncthreads();
+    if (part == 0 && k < K) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += sh[i][lane];
+        dgain[k] = s;
+    }
+}
+
+}  // namespace sbl

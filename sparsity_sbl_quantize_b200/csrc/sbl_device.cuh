@@ -18,6 +18,7 @@ enum : uint32_t {
     kErrDecode = 1u << 3,
     kErrPack = 1u << 4,
     kErrGemv = 1u << 5,
+    kErrB8Gemm = 1u << 6,
 };
 
 // Every device-side wait gives up after this long and records an error.

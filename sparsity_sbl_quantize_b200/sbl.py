@@ -27,6 +27,9 @@ SBL_OK = 0
 SBL_FMT_PK2, SBL_FMT_NM, SBL_FMT_I8, SBL_FMT_BF16T, SBL_FMT_SP24, SBL_FMT_T24 = 1, 2, 4, 8, 16, 32
 SBL_BUF_MAIN, SBL_BUF_NM_BITMAP, SBL_BUF_SP24_META, SBL_BUF_T24_HI = 0, 1, 2, 3
 SBL_OP_QUANTIZE_MASK_PACK, SBL_OP_BACKWARD = 0, 1
+SBL_B8_E4M3, SBL_B8_E5M2, SBL_B8_I8 = 0, 1, 2
+SBL_B8_ROWS, SBL_B8_TILES = 0, 1
+SBL_ACT_SILU, SBL_ACT_RELU2 = 0, 1
 
 STATUS_NAMES = {0: "SBL_OK", 1: "SBL_ERR_INVALID_ARG", 2: "SBL_ERR_SHAPE", 3: "SBL_ERR_ALIGNMENT",
                 4: "SBL_ERR_UNSUPPORTED", 5: "SBL_ERR_WORKSPACE", 6: "SBL_ERR_CUDA",
@@ -44,6 +47,14 @@ class sbl_packed(ctypes.Structure):
                 ("bf16t", ctypes.c_void_p), ("gamma", ctypes.c_void_p),
                 ("sp24_values", ctypes.c_void_p), ("sp24_meta", ctypes.c_void_p),
                 ("t24_lo", ctypes.c_void_p), ("t24_hi", ctypes.c_void_p)]
+
+
+class sbl_b8_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
+class sbl_b8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 class sbl_pack_variant(ctypes.Structure):
@@ -145,6 +156,25 @@ _lib.sbl_container_info.restype = ctypes.c_int
 _lib.sbl_container_info.argtypes = [_P, _sz, _D, ctypes.POINTER(_u32), ctypes.POINTER(ctypes.c_float)]
 _lib.sbl_container_read.restype = ctypes.c_int
 _lib.sbl_container_read.argtypes = [_P, _sz, ctypes.POINTER(sbl_host_buffers)]
+_B, _M = ctypes.POINTER(sbl_b8_desc), ctypes.POINTER(sbl_b8)
+_i64 = ctypes.c_int64
+for _name, _args in {
+        "sbl_b8_quantize": [_B, _P, _i32, _i64, ctypes.c_int, _M, _M, _P],
+        "sbl_b8_transpose": [_B, _M, _i32, _M, _P],
+        "sbl_b8_dequantize": [_B, _M, _P, _i64, _P],
+        "sbl_b8_gemm": [_B, _M, _B, _M, _P, _i64, _i32, _i32, _P],
+        "sbl_b8_linear_forward": [_B, _M, _P, _i64, _i32, _i32, _M, _P, _i64, _i32, _P],
+        "sbl_b8_linear_backward": [_B, _M, _M, _i32, _P, _i64, _i32, _i32, _P, _i32, _P, _i32, _P, _sz, _P],
+        "sbl_glu_forward": [_B, ctypes.c_int, _P, _i64, _P, _i64, _P, _i64, _M, _M, _P],
+        "sbl_glu_backward": [_B, ctypes.c_int, _M, _M, _P, _i64, _P, _i64, _P, _i64, _P],
+        "sbl_quantize_act_rmsnorm_checkpoint": [_B, _P, _P, ctypes.c_double, _P, _P, _M, _P],
+        "sbl_rmsnorm_backward": [_B, _M, _P, ctypes.c_double, _P, _P, _P, _P, _P, _sz, _P]}.items():
+    getattr(_lib, _name).restype = ctypes.c_int
+    getattr(_lib, _name).argtypes = _args
+for _name, _args in {"sbl_b8_row_bytes": [_B], "sbl_b8_scale_bytes": [_B], "sbl_b8_linear_workspace_bytes": [_B, _i32],
+                     "sbl_rmsnorm_backward_workspace_bytes": [_i32, _i32]}.items():
+    getattr(_lib, _name).restype = _sz
+    getattr(_lib, _name).argtypes = _args
 
 EXPORTED = ["sbl_status_string", "sbl_version", "sbl_packed_row_bytes", "sbl_workspace_bytes",
             "sbl_quantize_mask_pack", "sbl_quantize_mask_pack_stats", "sbl_quantize_mask_pack_noalloc", "sbl_quantize_act", "sbl_quantize_act_rmsnorm", "sbl_forward", "sbl_linear_forward",
@@ -154,7 +184,11 @@ EXPORTED = ["sbl_status_string", "sbl_version", "sbl_packed_row_bytes", "sbl_wor
             "sbl_backward_dual_ste", "sbl_backward_dual_ste_ex",
             "sbl_quantize_mask_pack_ex", "sbl_device_error", "sbl_selftest_wait_expiry", "sbl_container_bytes",
             "sbl_container_write",
-            "sbl_container_info", "sbl_container_read"]
+            "sbl_container_info", "sbl_container_read",
+            "sbl_b8_row_bytes", "sbl_b8_scale_bytes", "sbl_b8_quantize", "sbl_b8_transpose", "sbl_b8_dequantize",
+            "sbl_b8_gemm", "sbl_b8_linear_forward", "sbl_b8_linear_workspace_bytes", "sbl_b8_linear_backward",
+            "sbl_glu_forward", "sbl_glu_backward", "sbl_quantize_act_rmsnorm_checkpoint",
+            "sbl_rmsnorm_backward_workspace_bytes", "sbl_rmsnorm_backward"]
 
 
 class SblError(RuntimeError):
@@ -359,6 +393,128 @@ SBL_DEVICE_ERROR_SELFTEST = 0x80000000
 def sbl_selftest_wait_expiry() -> None:
     """Enqueue the bounded-wait self-test; its bit appears in sbl_device_error."""
     _check(_lib.sbl_selftest_wait_expiry(_stream()), "sbl_selftest_wait_expiry")
+
+
+# ------------------------------------------------------ 8-bit block matrices
+
+@dataclass
+class Block8:
+    """Device buffers of one b8 matrix: codes [rows, row bytes], scales (bytes in the library's order)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    def c(self) -> sbl_b8:
+        return sbl_b8(self.codes.data_ptr(), self.scales.data_ptr())
+
+
+def b8_desc(rows: int, cols: int, type: int = SBL_B8_E4M3) -> sbl_b8_desc:
+    return sbl_b8_desc(rows, cols, type)
+
+
+def _b8ref(m: Optional[Block8]):
+    return ctypes.byref(m.c()) if m is not None else None
+
+
+def _ld(t: Optional[torch.Tensor]) -> int:
+    """Row stride in elements of a matrix whose rows are contiguous."""
+    if t is None:
+        return 0
+    if t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError("a 2-D tensor with contiguous rows is needed")
+    return t.stride(0) if t.size(0) > 1 else t.size(1)
+
+
+def _fp32(t: Optional[torch.Tensor]) -> int:
+    return 1 if t is not None and t.dtype == torch.float32 else 0
+
+
+def sbl_b8_row_bytes(d: sbl_b8_desc) -> int:
+    return int(_lib.sbl_b8_row_bytes(ctypes.byref(d)))
+
+
+def sbl_b8_scale_bytes(d: sbl_b8_desc) -> int:
+    return int(_lib.sbl_b8_scale_bytes(ctypes.byref(d)))
+
+
+def alloc_b8(d: sbl_b8_desc, device="cuda") -> Block8:
+    """Allocate (with torch) the buffers of a b8 matrix."""
+    return Block8(codes=torch.empty((d.rows, sbl_b8_row_bytes(d)), dtype=torch.uint8, device=device),
+                  scales=torch.empty(sbl_b8_scale_bytes(d), dtype=torch.uint8, device=device))
+
+
+def sbl_b8_quantize(d: sbl_b8_desc, X: torch.Tensor, out: Optional[Block8], out_t: Optional[Block8] = None,
+                    blocks: int = SBL_B8_ROWS) -> None:
+    """X (bf16 or fp32, any row stride) -> out and / or its transpose out_t."""
+    _check(_lib.sbl_b8_quantize(ctypes.byref(d), _ptr(X), _fp32(X), _ld(X), blocks, _b8ref(out), _b8ref(out_t),
+                                _stream()), "sbl_b8_quantize")
+
+
+def sbl_b8_transpose(d: sbl_b8_desc, src: Block8, out_t: Block8, type_t: Optional[int] = None) -> None:
+    _check(_lib.sbl_b8_transpose(ctypes.byref(d), _b8ref(src), d.type if type_t is None else type_t, _b8ref(out_t),
+                                 _stream()), "sbl_b8_transpose")
+
+
+def sbl_b8_dequantize(d: sbl_b8_desc, src: Block8, X: torch.Tensor) -> None:
+    _check(_lib.sbl_b8_dequantize(ctypes.byref(d), _b8ref(src), _ptr(X), _ld(X), _stream()), "sbl_b8_dequantize")
+
+
+def sbl_b8_gemm(ad: sbl_b8_desc, a: Block8, bd: sbl_b8_desc, b: Block8, D: torch.Tensor, accumulate: bool = False) -> None:
+    """D [a rows, b rows] (bf16 or fp32) = or += a b^T."""
+    _check(_lib.sbl_b8_gemm(ctypes.byref(ad), _b8ref(a), ctypes.byref(bd), _b8ref(b), _ptr(D), _ld(D), _fp32(D),
+                            1 if accumulate else 0, _stream()), "sbl_b8_gemm")
+
+
+def sbl_b8_linear_forward(wd: sbl_b8_desc, w: Block8, X: torch.Tensor, T: int, xq: Block8, Y: torch.Tensor,
+                          x_type: int = SBL_B8_E4M3) -> None:
+    """X (bf16) -> its 8-bit form xq (the backward's checkpoint) and Y = xq w^T (bf16 or fp32)."""
+    _check(_lib.sbl_b8_linear_forward(ctypes.byref(wd), _b8ref(w), _ptr(X), _ld(X), T, x_type, _b8ref(xq), _ptr(Y),
+                                      _ld(Y), _fp32(Y), _stream()), "sbl_b8_linear_forward")
+
+
+def sbl_b8_linear_workspace_bytes(wd: sbl_b8_desc, T: int) -> int:
+    return int(_lib.sbl_b8_linear_workspace_bytes(ctypes.byref(wd), T))
+
+
+def sbl_b8_linear_backward(wd: sbl_b8_desc, w_t: Optional[Block8], xq: Optional[Block8], dY: torch.Tensor, T: int,
+                           dX: Optional[torch.Tensor], dW: Optional[torch.Tensor], workspace: Optional[torch.Tensor],
+                           x_type: int = SBL_B8_E4M3, g_type: int = SBL_B8_E4M3, accumulate: bool = False) -> None:
+    """dX (bf16 or fp32) and dW (fp32, added to when accumulate) from the checkpoint xq."""
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.sbl_b8_linear_backward(ctypes.byref(wd), _b8ref(w_t), _b8ref(xq), x_type, _ptr(dY), _ld(dY), T, g_type,
+                                       _ptr(dX), _fp32(dX), _ptr(dW), 1 if accumulate else 0, _ptr(workspace), nbytes,
+                                       _stream()), "sbl_b8_linear_backward")
+
+
+def sbl_glu_forward(d: sbl_b8_desc, act: int, G: torch.Tensor, U: Optional[torch.Tensor], H: Optional[torch.Tensor],
+                    g8: Optional[Block8] = None, u8: Optional[Block8] = None) -> None:
+    """H = act(G) * U and the checkpoints of G and U; every output optional."""
+    _check(_lib.sbl_glu_forward(ctypes.byref(d), act, _ptr(G), _ld(G), _ptr(U), _ld(U), _ptr(H), _ld(H), _b8ref(g8),
+                                _b8ref(u8), _stream()), "sbl_glu_forward")
+
+
+def sbl_glu_backward(d: sbl_b8_desc, act: int, g8: Block8, u8: Optional[Block8], dH: torch.Tensor, dG: torch.Tensor,
+                     dU: Optional[torch.Tensor]) -> None:
+    _check(_lib.sbl_glu_backward(ctypes.byref(d), act, _b8ref(g8), _b8ref(u8), _ptr(dH), _ld(dH), _ptr(dG), _ld(dG),
+                                 _ptr(dU), _ld(dU), _stream()), "sbl_glu_backward")
+
+
+def sbl_quantize_act_rmsnorm_checkpoint(d: sbl_b8_desc, X: torch.Tensor, g: Optional[torch.Tensor], eps: float,
+                                        Xq: torch.Tensor, dscale: torch.Tensor, x8: Block8) -> None:
+    _check(_lib.sbl_quantize_act_rmsnorm_checkpoint(ctypes.byref(d), _ptr(X), _ptr(g), float(eps), _ptr(Xq), _ptr(dscale),
+                                                    _b8ref(x8), _stream()), "sbl_quantize_act_rmsnorm_checkpoint")
+
+
+def sbl_rmsnorm_backward_workspace_bytes(T: int, K: int) -> int:
+    return int(_lib.sbl_rmsnorm_backward_workspace_bytes(T, K))
+
+
+def sbl_rmsnorm_backward(d: sbl_b8_desc, x8: Block8, g: Optional[torch.Tensor], eps: float, dU: torch.Tensor,
+                         dR: Optional[torch.Tensor], dX: torch.Tensor, dg: Optional[torch.Tensor],
+                         workspace: Optional[torch.Tensor]) -> None:
+    """dX (+ dR) and the gains' gradient dg from the checkpointed norm input x8."""
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.sbl_rmsnorm_backward(ctypes.byref(d), _b8ref(x8), _ptr(g), float(eps), _ptr(dU), _ptr(dR), _ptr(dX),
+                                     _ptr(dg), _ptr(workspace), nbytes, _stream()), "sbl_rmsnorm_backward")
 
 
 # ------------------------------------------------- allocation helpers (torch)
