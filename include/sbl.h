@@ -628,10 +628,12 @@ sbl_status sbl_glu_forward(const sbl_b8_desc *desc, sbl_activation act, const ui
 sbl_status sbl_glu_backward(const sbl_b8_desc *desc, sbl_activation act, const sbl_b8 *g8, const sbl_b8 *u8, const uint16_t *dH,
                             int64_t lddh, uint16_t *dG, int64_t lddg, uint16_t *dU, int64_t lddu, void *stream);
 
-/* sbl_quantize_act_rmsnorm (same Xq, d bit for bit) that also writes the
- * checkpoint x8 of X; desc: {T, K, checkpoint type}.  eps is a double here (the
- * statistic is computed in fp64; the other entry point's fp32 eps widened gives
- * its results).  One launch. */
+/* sbl_quantize_act_rmsnorm that also writes the checkpoint x8 of X; desc: {T, K,
+ * checkpoint type}.  u, a_t and d are those of the other entry point for the same
+ * eps (a double here, as the statistic is computed in fp64).  The quantisation
+ * factor is formed as fl32(127 * fl32(1 / a_t)) instead of fl32(127 / a_t), so a
+ * code differs from the other entry point's by one where its scaled value lies
+ * within 2^-22 of a tie (a few values in a million).  One launch. */
 sbl_status sbl_quantize_act_rmsnorm_checkpoint(const sbl_b8_desc *desc, const uint16_t *X, const uint16_t *g, double eps,
                                                int8_t *Xq, float *d, const sbl_b8 *x8, void *stream);
 

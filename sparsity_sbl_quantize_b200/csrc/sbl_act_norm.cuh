@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 3)
     for (int w = 1; w < W; ++w) amax = fmaxf(amax, wmax[sub][w]);
     if (!active) return;
     const bool zero = !(amax > 0.0f);
-    const float rq = zero ? 0.0f : __fdiv_rn(127.0f, amax);
+    // with a checkpoint the factor is 127 * (1 / a), two roundings (sbl.h)
+    const float rq = zero ? 0.0f : CK == kNoCkpt ? __fdiv_rn(127.0f, amax) : __fmul_rn(127.0f, __frcp_rn(amax));
 #pragma unroll
     for (int c = 0; c < kActMaxChunks; ++c) {
         const int ci = lt + c * RT;

@@ -24,8 +24,10 @@ struct B8RowArgs {
 template <int TYPE, int SRC>
 __global__ void __launch_bounds__(256) b8_quantize_rows_kernel(B8RowArgs a)
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // in this order: a kernel launched after this one may read, before its own
+    // wait, whatever was final when this one began (the product reads W)
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, half = lane >> 4;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int64_t row = unit / a.words;

@@ -12,6 +12,7 @@
 #include "sbl_act_norm.cuh"
 #include "sbl_b8.cuh"
 #include "sbl_b8_gemm.cuh"
+#include "sbl_b8_skinny.cuh"
 #include "sbl_ckpt.cuh"
 #include "sbl_host.h"
 
@@ -33,9 +34,25 @@ static sbl_status b8_device(HostDevice *hd)
     if (st != SBL_OK) return st;
     std::lock_guard<std::mutex> lock(g_b8_mutex);
     if (!g_b8_ready[hd->index]) {
-        if (cudaFuncSetAttribute(b8_gemm_kernel<128, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 B8Cfg<128, false>::kSmemBytes) != cudaSuccess)
-            return SBL_ERR_CUDA;
+        sbl_status st2 = SBL_OK;
+        auto allow = [&](auto kernel) {
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kB8SmemAll) != cudaSuccess) st2 = SBL_ERR_CUDA;
+        };
+        allow(b8_gemm_kernel<128, false, false>);
+        allow(b8_gemm_kernel<128, false, true>);
+        allow(b8_gemm_kernel<256, true, false>);
+        allow(b8_gemm_kernel<256, true, true>);
+        allow(b8_skinny_kernel<kB8E4M3, 16, true>);
+        allow(b8_skinny_kernel<kB8E4M3, 32, true>);
+        allow(b8_skinny_kernel<kB8E4M3, 64, true>);
+        allow(b8_skinny_kernel<kB8E5M2, 16, true>);
+        allow(b8_skinny_kernel<kB8E5M2, 32, true>);
+        allow(b8_skinny_kernel<kB8E5M2, 64, true>);
+        allow(b8_skinny_kernel<0, 16, false>);
+        allow(b8_skinny_kernel<0, 32, false>);
+        allow(b8_skinny_kernel<0, 64, false>);
+        allow(b8_skinny_kernel<0, 128, false>);
+        if (st2 != SBL_OK) return st2;
         g_b8_ready[hd->index] = true;
     }
     return SBL_OK;
@@ -212,7 +229,7 @@ static bool encode_scales(const HostDevice &hd, CUtensorMap *map, const sbl_b8_d
                      CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-template <int BN, bool PAIR>
+template <int BN, bool PAIR, bool LONG>
 static sbl_status launch_b8_gemm(const HostDevice &hd, const sbl_b8_desc *ad, const sbl_b8 *A, const sbl_b8_desc *bd, const sbl_b8 *B,
                                  void *D, int64_t ldd, B8GemmArgs args, cudaStream_t stream)
 {
@@ -248,13 +265,126 @@ static sbl_status launch_b8_gemm(const HostDevice &hd, const sbl_b8_desc *ad, co
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, b8_gemm_kernel<BN, PAIR>, ta, tb, tsa, tsb, ty, args) != cudaSuccess) return SBL_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, b8_gemm_kernel<BN, PAIR, LONG>, ta, tb, tsa, tsb, ty, args) != cudaSuccess) return SBL_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SBL_OK : SBL_ERR_CUDA;
+}
+
+// How the product of few tokens runs: padded tokens, CTAs that share K, stages.
+struct SkinnyPlan {
+    int nt, split, stages, max_blocks, max_groups, tmem_cols;
+    int64_t smem;
+};
+
+static SkinnyPlan skinny_plan(int num_sms, int32_t O, int32_t K, int32_t T, bool fused)
+{
+    SkinnyPlan p;
+    p.nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+    const int64_t tiles = (O + kBM - 1) / kBM;
+    const int blocks = (K + 127) / 128;
+    // Enough CTAs for every SM, two blocks each at least.  More of them
+    // measured slower (6912 x 2560: 216 CTAs 7.1 us, 432 11.3).
+    p.split = 1;
+    while (p.split < kSkMaxSplit && tiles * p.split < num_sms && blocks >= 4 * p.split) p.split *= 2;
+    p.max_blocks = (blocks + p.split - 1) / p.split;
+    p.max_groups = (p.max_blocks + 2) / 4 + 1;
+    // As many stages as fit when the CTAs of one round share the SMs, two to
+    // an SM at least: at one to an SM the clusters of eight do not all find
+    // room at once (2048 x 11008: 15.1 us instead of 7.9).
+    const int64_t ctas = std::min<int64_t>(std::max<int64_t>((tiles * p.split + num_sms - 1) / num_sms, 2), 4);
+    const int64_t fixed = 1024 + (fused ? static_cast<int64_t>(p.max_blocks) * p.nt * kBKBytes : 0) + 1024 * p.max_groups + 512;
+    const int64_t room = (kB8SmemAll - 1024 * ctas) / ctas - fixed;
+    p.stages = static_cast<int>(std::max<int64_t>(2, std::min<int64_t>({p.max_blocks, room / skinny_stage_bytes(p.nt, fused), kSkMaxStages})));
+    p.tmem_cols = 32;
+    while (p.tmem_cols < p.nt + 8 * p.max_groups) p.tmem_cols *= 2;
+    p.smem = fixed + p.stages * skinny_stage_bytes(p.nt, fused);
+    // shared memory in proportion to tensor memory (see kB8SmemAll)
+    p.smem = std::max<int64_t>(p.smem, static_cast<int64_t>(p.tmem_cols) * kB8SmemAll / kTmemCols);
+    return p;
+}
+
+template <int TYPE, int NT, bool FUSED>
+static sbl_status launch_skinny_nt(const HostDevice &hd, const SkinnyPlan &p, const sbl_b8_desc *wd, const sbl_b8 *W, const sbl_b8_desc *xd,
+                                   const sbl_b8 *xq, SkinnyArgs a, cudaStream_t stream)
+{
+    CUtensorMap tw, tx;
+    memset(&tx, 0, sizeof(tx));
+    if (!encode_codes(hd, &tw, wd, W, kBM) || (!FUSED && !encode_codes(hd, &tx, xd, xq, NT))) return SBL_ERR_CUDA;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(static_cast<unsigned>((wd->rows + kBM - 1) / kBM * p.split));
+    cfg.blockDim = dim3(kSkThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, b8_skinny_kernel<TYPE, NT, FUSED>, tw, tx, a) != cudaSuccess) return SBL_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? SBL_OK : SBL_ERR_CUDA;
+}
+
+// Y [T, O] = X W^T for few tokens.  X: bf16 (quantised in the kernel, xq an
+// output) or nullptr (xq an input).
+static sbl_status skinny(const HostDevice &hd, const SkinnyPlan &p, const sbl_b8_desc *wd, const sbl_b8 *W, const sbl_b8_desc *xd,
+                         const uint16_t *X, int64_t ldx, const sbl_b8 *xq, void *Y, int64_t ldy, bool fp32, bool accumulate, bool w_early, cudaStream_t stream)
+{
+    SkinnyArgs a;
+    memset(&a, 0, sizeof(a));
+    a.O = wd->rows;
+    a.K = wd->cols;
+    a.T = xd->rows;
+    a.blocks = (a.K + 127) / 128;
+    a.split = p.split;
+    a.stages = p.stages;
+    a.max_groups = p.max_groups;
+    a.max_blocks = p.max_blocks;
+    a.tmem_cols = static_cast<uint32_t>(p.tmem_cols);
+    a.idesc = b8_idesc(wd->type, xd->type, kBM, p.nt);
+    a.X = X;
+    a.ldx = ldx;
+    a.xc = xq->codes;
+    a.ldc = b8_ld(xd);
+    a.xs = scale_words(xq);
+    a.xrp = b8_rp(xd->rows);
+    a.words = b8_words(xd->cols);
+    a.ws = scale_words(W);
+    a.wrp = b8_rp(wd->rows);
+    a.Y = Y;
+    a.ldy = ldy;
+    a.y_fp32 = fp32 ? 1 : 0;
+    a.accumulate = accumulate ? 1 : 0;
+    a.w_early = w_early ? 1 : 0;
+    a.err = hd.err;
+    const bool e5 = xd->type == SBL_B8_E5M2;
+    if (!X) {
+        switch (p.nt) {
+        case 16: return launch_skinny_nt<0, 16, false>(hd, p, wd, W, xd, xq, a, stream);
+        case 32: return launch_skinny_nt<0, 32, false>(hd, p, wd, W, xd, xq, a, stream);
+        case 64: return launch_skinny_nt<0, 64, false>(hd, p, wd, W, xd, xq, a, stream);
+        default: return launch_skinny_nt<0, 128, false>(hd, p, wd, W, xd, xq, a, stream);
+        }
+    }
+    switch (p.nt) {
+    case 16:
+        return e5 ? launch_skinny_nt<kB8E5M2, 16, true>(hd, p, wd, W, xd, xq, a, stream)
+                  : launch_skinny_nt<kB8E4M3, 16, true>(hd, p, wd, W, xd, xq, a, stream);
+    case 32:
+        return e5 ? launch_skinny_nt<kB8E5M2, 32, true>(hd, p, wd, W, xd, xq, a, stream)
+                  : launch_skinny_nt<kB8E4M3, 32, true>(hd, p, wd, W, xd, xq, a, stream);
+    default:
+        return e5 ? launch_skinny_nt<kB8E5M2, 64, true>(hd, p, wd, W, xd, xq, a, stream)
+                  : launch_skinny_nt<kB8E4M3, 64, true>(hd, p, wd, W, xd, xq, a, stream);
+    }
 }
 
 // D = A B^T; every argument checked.
 static sbl_status gemm(const HostDevice &hd, const sbl_b8_desc *ad, const sbl_b8 *A, const sbl_b8_desc *bd, const sbl_b8 *B, void *D,
-                       int64_t ldd, bool fp32, bool accumulate, cudaStream_t stream)
+                       int64_t ldd, bool fp32, bool accumulate, bool w_early, cudaStream_t stream)
 {
     B8GemmArgs args;
     memset(&args, 0, sizeof(args));
@@ -263,7 +393,29 @@ static sbl_status gemm(const HostDevice &hd, const sbl_b8_desc *ad, const sbl_b8
     args.k_blocks = (ad->cols + 127) / 128;
     args.out_fp32 = fp32 ? 1 : 0;
     args.accumulate = accumulate ? 1 : 0;
-    return launch_b8_gemm<128, false>(hd, ad, A, bd, B, D, ldd, args, stream);
+    // Few rows: the kernel that splits K.  It measured faster up to 64 rows
+    // (6912 x 2560 at 64: 9.1 us against 11.0; 2560 x 6912: 9.5 against 23.5),
+    // and to 128 only where the other's tiles leave most SMs idle (2560 x 6912 at
+    // 128: 11.6 against 23.8; 11008 x 2048: 13.4 against 10.4).
+    const int64_t tiles_w = (args.N + kBM - 1) / kBM;
+    if (args.M <= 64 || (args.M <= 128 && 4 * tiles_w <= hd.num_sms)) {
+        const SkinnyPlan p = skinny_plan(hd.num_sms, bd->rows, bd->cols, ad->rows, false);
+        if (!fp32 || p.max_blocks <= kB8SegBlocks)  // longer fp32 sums: see LONG
+            return skinny(hd, p, bd, B, ad, nullptr, 0, A, D, ldd, fp32, accumulate, w_early, stream);
+    }
+    // 256 x 256 tiles on CTA pairs or 128 x 128 ones on single CTAs: the time
+    // of a launch in units of 0.2 us fits 20 + 2.5 rounds blocks for the
+    // first, 15 + 2 rounds blocks for the second (16384 x 2048 x 11008: 290 against
+    // 473 us; 512 x 6912 x 2560: 13.9 against 19.2; 300 x 4864 x 896: 7.9 against 6.1).
+    auto rounds = [](int64_t m, int64_t n, int64_t t, int64_t units) { return ((m + t - 1) / t * ((n + t - 1) / t) + units - 1) / units; };
+    const int64_t pair_cost = 40 + 5 * rounds(args.M, args.N, 256, hd.num_sms / 2) * args.k_blocks;
+    const int64_t one_cost = 30 + 4 * rounds(args.M, args.N, 128, hd.num_sms) * args.k_blocks;
+    const bool lng = fp32 && args.k_blocks > kB8SegBlocks;
+    if (pair_cost <= one_cost)
+        return lng ? launch_b8_gemm<256, true, true>(hd, ad, A, bd, B, D, ldd, args, stream)
+                   : launch_b8_gemm<256, true, false>(hd, ad, A, bd, B, D, ldd, args, stream);
+    return lng ? launch_b8_gemm<128, false, true>(hd, ad, A, bd, B, D, ldd, args, stream)
+               : launch_b8_gemm<128, false, false>(hd, ad, A, bd, B, D, ldd, args, stream);
 }
 
 // The workspace of sbl_b8_linear_backward: dY in both block orders and X
@@ -456,7 +608,7 @@ sbl_status sbl_b8_gemm(const sbl_b8_desc *a_desc, const sbl_b8 *a, const sbl_b8_
     if (!b8_aligned(a) || !b8_aligned(b)) return SBL_ERR_ALIGNMENT;
     HostDevice hd;
     if ((st = b8_device(&hd)) != SBL_OK) return st;
-    return gemm(hd, a_desc, a, b_desc, b, D, ldd, d_is_fp32 != 0, accumulate != 0, static_cast<cudaStream_t>(stream));
+    return gemm(hd, a_desc, a, b_desc, b, D, ldd, d_is_fp32 != 0, accumulate != 0, false, static_cast<cudaStream_t>(stream));
 }
 
 // W [O, K] of a b8 linear: both sizes multiples of 16 up to 65536, a product type.
@@ -485,8 +637,17 @@ sbl_status sbl_b8_linear_forward(const sbl_b8_desc *w_desc, const sbl_b8 *w, con
     HostDevice hd;
     if ((st = b8_device(&hd)) != SBL_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // One launch that quantises X itself while each CTA's share of it is
+    // small: 64 (token, block) pairs measured even with two launches
+    // (6912 x 2560: 1 token 7.2 us against 8.9, 13 tokens 9.4 against 9.5;
+    // 2560 x 6912: 8 tokens, 56 pairs, 8.9 against 10.1, 13 tokens 10.8 against 10.3).
+    if (T <= 64) {
+        const SkinnyPlan p = skinny_plan(hd.num_sms, w_desc->rows, w_desc->cols, T, true);
+        if (p.smem <= kB8SmemAll && static_cast<int64_t>(T) * p.max_blocks <= 64 && !(y_is_fp32 && p.max_blocks > kB8SegBlocks))
+            return skinny(hd, p, w_desc, w, &xd, X, ldx, xq, Y, ldy, y_is_fp32 != 0, false, false, s);
+    }
     if ((st = quantize(&xd, X, false, ldx, false, xq, nullptr, s)) != SBL_OK) return st;
-    return gemm(hd, &xd, xq, w_desc, w, Y, ldy, y_is_fp32 != 0, false, s);
+    return gemm(hd, &xd, xq, w_desc, w, Y, ldy, y_is_fp32 != 0, false, true, s);
 }
 
 size_t sbl_b8_linear_workspace_bytes(const sbl_b8_desc *w_desc, int32_t T)
@@ -527,11 +688,11 @@ sbl_status sbl_b8_linear_backward(const sbl_b8_desc *w_desc, const sbl_b8 *w_t, 
     if ((st = quantize(&gd, dY, false, lddy, false, dX ? &g : nullptr, dW ? &gt : nullptr, s)) != SBL_OK) return st;
     if (dX) {
         const sbl_b8_desc wt = {K, O, w_desc->type};
-        if ((st = gemm(hd, &p.g, &g, &wt, w_t, dX, K, dx_is_fp32 != 0, false, s)) != SBL_OK) return st;
+        if ((st = gemm(hd, &p.g, &g, &wt, w_t, dX, K, dx_is_fp32 != 0, false, false, s)) != SBL_OK) return st;
     }
     if (dW) {
         if ((st = transpose(&xd, xq, x_type, &xt, s)) != SBL_OK) return st;
-        if ((st = gemm(hd, &p.gt, &gt, &p.xt, &xt, dW, K, true, dw_accumulate != 0, s)) != SBL_OK) return st;
+        if ((st = gemm(hd, &p.gt, &gt, &p.xt, &xt, dW, K, true, dw_accumulate != 0, false, s)) != SBL_OK) return st;
     }
     return SBL_OK;
 }

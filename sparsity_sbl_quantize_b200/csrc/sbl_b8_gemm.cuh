@@ -19,6 +19,7 @@
 
 #include <cuda_bf16.h>
 
+#include "sbl_b8_format.cuh"
 #include "sbl_device.cuh"
 #include "sbl_gemm.cuh"  // tile raster, role sizes
 
@@ -40,6 +41,13 @@ struct B8GemmArgs {
 // ring holds, so a copy never meets MMAs that still read the old scales.
 constexpr int kB8SfBufs = 4;
 
+// A kernel that takes c of the 512 columns of tensor memory takes at least
+// c / 512 of the SM's shared memory too (all of it here).  Then CTAs that fit
+// on an SM together also find their tensor memory, whatever kernels and
+// streams they belong to: an allocation that had to wait for another CTA,
+// while both wait for cluster mates elsewhere, could close a circle.
+constexpr int kB8SmemAll = 227 * 1024;
+
 template <int BN, bool PAIR>
 struct B8Cfg {
     static_assert(BN == 128 || BN == 256, "tile width");
@@ -57,7 +65,8 @@ struct B8Cfg {
     static constexpr int kAcc1 = 2 * BN <= kSfCol0 ? BN : (kSfCol0 - BN) / 32 * 32;
     static constexpr int kOverlap = BN - kAcc1;  // columns shared by the accumulators
     static_assert(kOverlap <= 64, "the first drained columns must free the overlap");
-    static constexpr int kSmemBytes = 1024 + kStages * (kStageBytes + kSfBytes) + kEpiBytes + 256;
+    static_assert(1024 + kStages * (kStageBytes + kSfBytes) + kEpiBytes + 256 <= kB8SmemAll, "shared memory");
+    static constexpr int kSmemBytes = kB8SmemAll;
 };
 
 // Instruction descriptor of kind::mxf8f6f4: B scale id (bits 4-5), A / B type
@@ -122,9 +131,19 @@ __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap *map, uint32
                  : "memory");
 }
 
+// K blocks summed in tensor memory before the sum moves to registers (LONG).
+constexpr int kB8SegBlocks = 32;
+
+// LONG: fp32 results of long reductions.  The tensor core truncates when it
+// adds to its accumulator, so the error of a sum of n steps grows with n
+// (relative to the result, measured on random operands: 1.0e-7 at K = 2048,
+// 4.8e-7 at 8192, 1.2e-6 at 16384, where rounded additions give 1.9e-7).  The
+// reduction is therefore cut into segments of kB8SegBlocks blocks, each
+// summed in tensor memory and then added in registers with rounding.
+//
 // tmSA, tmSB: the scale words as [ceil(blocks / 4), padded rows] of 32 bits,
 // boxes of 128 (A) and BN (B) words: both CTAs of a pair need every B scale.
-template <int BN, bool PAIR>
+template <int BN, bool PAIR, bool LONG>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     b8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
@@ -156,6 +175,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const bool leader = rank == 0;
     const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
     const int units = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
+    const int segments = LONG ? (args.k_blocks + kB8SegBlocks - 1) / kB8SegBlocks : 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -250,66 +270,70 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         bool ok = true;
         int local = 0;
         uint32_t sf_group = 0;  // groups of four stages so far
-        for (int tile = unit; ok && tile < num_tiles; tile += units, ++local) {
-            const int acc = local & 1;
-            // The accumulator's columns are free: with two disjoint ones when
-            // tile local - 2 is drained; with overlapping ones when the first
-            // columns of tile local - 1 are (all of local - 2 is by then).
-            bool free_acc = true;
-            if constexpr (Cfg::kOverlap > 0) {
-                if (local >= 1)
-                    free_acc = mbar_wait(tempty_bar(acc ^ 1), ((local - 1) >> 1) & 1, args.err, kErrB8Gemm);
-            } else {
-                free_acc = mbar_wait(tempty_bar(acc), ((local >> 1) & 1) ^ 1, args.err, kErrB8Gemm);
-            }
-            if (!__all_sync(0xffffffffu, free_acc)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * Cfg::kAcc1);
-            uint32_t sfa = 0;
-            for (int kb = 0; kb < args.k_blocks; ++kb) {
-                const bool ready = mbar_wait(full_bar(stage), phase, args.err, kErrB8Gemm);
-                if (!__all_sync(0xffffffffu, ready)) {
+        for (int tile = unit; ok && tile < num_tiles; tile += units) {
+            for (int seg = 0; ok && seg < segments; ++seg, ++local) {
+                const int kb0 = LONG ? seg * kB8SegBlocks : 0;
+                const int kb1 = LONG ? min(kb0 + kB8SegBlocks, args.k_blocks) : args.k_blocks;
+                const int acc = local & 1;
+                // The accumulator's columns are free: with two disjoint ones when
+                // tile local - 2 is drained; with overlapping ones when the first
+                // columns of tile local - 1 are (all of local - 2 is by then).
+                bool free_acc = true;
+                if constexpr (Cfg::kOverlap > 0) {
+                    if (local >= 1)
+                        free_acc = mbar_wait(tempty_bar(acc ^ 1), ((local - 1) >> 1) & 1, args.err, kErrB8Gemm);
+                } else {
+                    free_acc = mbar_wait(tempty_bar(acc), ((local >> 1) & 1) ^ 1, args.err, kErrB8Gemm);
+                }
+                if (!__all_sync(0xffffffffu, free_acc)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if ((kb & 3) == 0) {
-                    sfa = tmem_base + Cfg::kSfCol0 + (sf_group % kB8SfBufs) * Cfg::kSfCols;
-                    ++sf_group;
-                }
-                if (lane == 0) {
-                    if ((kb & 3) == 0) {
-                        const uint32_t s = sf_base + stage * Cfg::kSfBytes;
-                        tmem_cp_scales<PAIR>(sfa, s);
-#pragma unroll
-                        for (int i = 0; i < BN / 128; ++i)
-                            tmem_cp_scales<PAIR>(sfa + 4 + 4 * i, s + Cfg::kSfaBytes + 512 * i);
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * Cfg::kAcc1);
+                uint32_t sfa = 0;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    const bool ready = mbar_wait(full_bar(stage), phase, args.err, kErrB8Gemm);
+                    if (!__all_sync(0xffffffffu, ready)) {
+                        ok = false;
+                        break;
                     }
-                    const uint32_t idesc = b8_idesc_with_block(args.idesc, kb);
-                    const uint64_t adesc = smem_desc_k128(a_base + stage * kABytes);
-                    const uint64_t bdesc = smem_desc_k128(b_base + stage * Cfg::kBBytes);
+                    tc_fence_after();
+                    if ((kb & 3) == 0) {
+                        sfa = tmem_base + Cfg::kSfCol0 + (sf_group % kB8SfBufs) * Cfg::kSfCols;
+                        ++sf_group;
+                    }
+                    if (lane == 0) {
+                        if ((kb & 3) == 0) {
+                            const uint32_t s = sf_base + stage * Cfg::kSfBytes;
+                            tmem_cp_scales<PAIR>(sfa, s);
 #pragma unroll
-                    for (int kk = 0; kk < kBKBytes / 32; ++kk)
-                        mma_b8<PAIR>(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, sfa, sfa + 4, (kb | kk) != 0);
+                            for (int i = 0; i < BN / 128; ++i)
+                                tmem_cp_scales<PAIR>(sfa + 4 + 4 * i, s + Cfg::kSfaBytes + 512 * i);
+                        }
+                        const uint32_t idesc = b8_idesc_with_block(args.idesc, kb);
+                        const uint64_t adesc = smem_desc_k128(a_base + stage * kABytes);
+                        const uint64_t bdesc = smem_desc_k128(b_base + stage * Cfg::kBBytes);
+#pragma unroll
+                        for (int kk = 0; kk < kBKBytes / 32; ++kk)
+                            mma_b8<PAIR>(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, sfa, sfa + 4, (kb > kb0 || kk > 0) ? 1u : 0u);
+                        if constexpr (PAIR)
+                            tc_commit_pair(empty_bar(stage), 0x3);
+                        else
+                            tc_commit(empty_bar(stage));
+                    }
+                    __syncwarp();
+                    if (++stage == kStages) stage = 0, phase ^= 1u;
+                }
+                if (!ok) break;
+                if (lane == 0) {
                     if constexpr (PAIR)
-                        tc_commit_pair(empty_bar(stage), 0x3);
+                        tc_commit_pair(tfull_bar(acc), 0x3);
                     else
-                        tc_commit(empty_bar(stage));
+                        tc_commit(tfull_bar(acc));
                 }
                 __syncwarp();
-                if (++stage == kStages) stage = 0, phase ^= 1u;
             }
-            if (!ok) break;
-            if (lane == 0) {
-                if constexpr (PAIR)
-                    tc_commit_pair(tfull_bar(acc), 0x3);
-                else
-                    tc_commit(tfull_bar(acc));
-            }
-            __syncwarp();
         }
         if (lane == 0) {
             if constexpr (PAIR)
@@ -332,78 +356,121 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         constexpr int kChunks = BN / 64;
         uint32_t nstore = 0;
         int local = 0;
-        for (int tile = unit; tile < num_tiles; tile += units, ++local) {
+        auto release = [&](int acc) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR)
+                    mbar_arrive_cluster(map_shared_rank(tempty_bar(acc), 0));
+                else
+                    mbar_arrive(tempty_bar(acc));
+            }
+        };
+        // 32 x 32 fp32 values of this warp to D (staged, swizzled, one TMA store)
+        auto store = [&](const uint32_t(&v)[32], int col, int row0) {
+            if (col >= args.N || row0 >= args.M) return;  // warp-uniform: block outside D
+            if (!args.out_fp32) {
+                // two 2 KiB staging halves in turn: rows of 64 bytes, chunk c
+                // at c ^ ((lane / 2) % 4) (64-byte swizzle)
+                const uint32_t sbuf = buf + static_cast<uint32_t>((nstore & 1) * (kEpiBufBytes / 2));
+                if (lane == 0) bulk_wait_group_read<1>();
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) w[q] = pack_bf16(__uint_as_float(v[8 * c + 2 * q]), __uint_as_float(v[8 * c + 2 * q + 1]));
+                    const uint32_t addr = sbuf + static_cast<uint32_t>(lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16));
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                 : "memory");
+                }
+            } else {
+                if (lane == 0) bulk_wait_group_read<0>();
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint32_t addr = buf + static_cast<uint32_t>(lane * 128 + ((c ^ (lane & 7)) * 16));
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[4 * c]), "r"(v[4 * c + 1]),
+                                 "r"(v[4 * c + 2]), "r"(v[4 * c + 3])
+                                 : "memory");
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (!args.out_fp32)
+                    tma_store_2d(&tmY, buf + static_cast<uint32_t>((nstore & 1) * (kEpiBufBytes / 2)), col, row0);
+                else if (args.accumulate)
+                    tma_reduce_add_2d(&tmY, buf, col, row0);
+                else
+                    tma_store_2d(&tmY, buf, col, row0);
+                bulk_commit_group();
+            }
+            ++nstore;
+        };
+        for (int tile = unit; tile < num_tiles; tile += units) {
             int tm, tn;
             tile_coords(tile, args.tiles_m, args.tiles_n, tm, tn);
-            const int acc = local & 1;
             const int row0 = tm * kTileM + static_cast<int>(rank) * kBM + quarter * 32;
-            const bool ready = mbar_wait(tfull_bar(acc), (local >> 1) & 1, args.err, kErrB8Gemm);
-            if (!__all_sync(0xffffffffu, ready)) break;
-            tc_fence_after();
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                   static_cast<uint32_t>(acc * Cfg::kAcc1 + 32 * half);
+            const int col0 = tn * BN + 32 * half;
+            if constexpr (LONG) {
+                float sum[kChunks][32];
+#pragma unroll
+                for (int j = 0; j < kChunks; ++j)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[j][i] = 0.0f;
+                bool ready = true;
+                for (int seg = 0; seg < segments; ++seg, ++local) {
+                    const int acc = local & 1;
+                    ready = __all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), (local >> 1) & 1, args.err, kErrB8Gemm));
+                    if (!ready) break;
+                    tc_fence_after();
+                    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                           static_cast<uint32_t>(acc * Cfg::kAcc1 + 32 * half);
+                    auto add = [&](int j, bool last) {
+                        uint32_t v[32];
+                        __syncwarp();
+                        tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(64 * j), v);
+                        tmem_wait_ld();
+                        if (last) release(acc);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) sum[j][i] = __fadd_rn(sum[j][i], __uint_as_float(v[i]));
+                    };
+                    constexpr int kFree = Cfg::kOverlap > 0 ? 0 : kChunks - 1;
+                    if (Cfg::kOverlap > 0 && acc == 0) {
+#pragma unroll
+                        for (int i = 0; i < kChunks; ++i) add(kChunks - 1 - i, i == kFree);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kChunks; ++i) add(i, i == kFree);
+                    }
+                }
+                if (!ready) break;
+#pragma unroll
+                for (int j = 0; j < kChunks; ++j) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sum[j][i]);
+                    store(v, col0 + 64 * j, row0);
+                }
+            } else {
+                const int acc = local & 1;
+                const bool ready = mbar_wait(tfull_bar(acc), (local >> 1) & 1, args.err, kErrB8Gemm);
+                if (!__all_sync(0xffffffffu, ready)) break;
+                tc_fence_after();
+                const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                       static_cast<uint32_t>(acc * Cfg::kAcc1 + 32 * half);
 #pragma unroll 1
-            for (int i = 0; i < kChunks; ++i) {
-                const int j = (Cfg::kOverlap > 0 && acc == 0) ? kChunks - 1 - i : i;
-                uint32_t v[32];
-                __syncwarp();
-                tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(64 * j), v);
-                tmem_wait_ld();
-                if (i == (Cfg::kOverlap > 0 ? 0 : kChunks - 1)) {
-                    tc_fence_before();
+                for (int i = 0; i < kChunks; ++i) {
+                    const int j = (Cfg::kOverlap > 0 && acc == 0) ? kChunks - 1 - i : i;
+                    uint32_t v[32];
                     __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (PAIR)
-                            mbar_arrive_cluster(map_shared_rank(tempty_bar(acc), 0));
-                        else
-                            mbar_arrive(tempty_bar(acc));
-                    }
+                    tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(64 * j), v);
+                    tmem_wait_ld();
+                    if (i == (Cfg::kOverlap > 0 ? 0 : kChunks - 1)) release(acc);
+                    store(v, col0 + 64 * j, row0);
                 }
-                const int col = tn * BN + 64 * j + 32 * half;
-                if (col >= args.N || row0 >= args.M) continue;  // warp-uniform: block outside D
-                if (!args.out_fp32) {
-                    // two 2 KiB staging halves in turn: rows of 64 bytes, chunk c
-                    // at c ^ ((lane / 2) % 4) (64-byte swizzle)
-                    const uint32_t sbuf = buf + static_cast<uint32_t>((nstore & 1) * (kEpiBufBytes / 2));
-                    if (lane == 0) bulk_wait_group_read<1>();
-                    __syncwarp();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[8 * c + 2 * q]),
-                                                                            __uint_as_float(v[8 * c + 2 * q + 1]));
-                            w[q] = *reinterpret_cast<const uint32_t *>(&b2);
-                        }
-                        const uint32_t addr = sbuf + static_cast<uint32_t>(lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16));
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]),
-                                     "r"(w[2]), "r"(w[3])
-                                     : "memory");
-                    }
-                } else {
-                    if (lane == 0) bulk_wait_group_read<0>();
-                    __syncwarp();
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const uint32_t addr = buf + static_cast<uint32_t>(lane * 128 + ((c ^ (lane & 7)) * 16));
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[4 * c]),
-                                     "r"(v[4 * c + 1]), "r"(v[4 * c + 2]), "r"(v[4 * c + 3])
-                                     : "memory");
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (!args.out_fp32)
-                        tma_store_2d(&tmY, buf + static_cast<uint32_t>((nstore & 1) * (kEpiBufBytes / 2)), col, row0);
-                    else if (args.accumulate)
-                        tma_reduce_add_2d(&tmY, buf, col, row0);
-                    else
-                        tma_store_2d(&tmY, buf, col, row0);
-                    bulk_commit_group();
-                }
-                ++nstore;
+                ++local;
             }
         }
         if (lane == 0) bulk_wait_group<0>();

@@ -204,13 +204,15 @@ def _check(status: int, call: str):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    """torch's current stream as a cudaStream_t.  The raw query costs 0.3 us
+    where building a torch.cuda.Stream costs 3.4, half of a small call."""
+    if torch.cuda.is_initialized():
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return torch.cuda.current_stream().cuda_stream  # initialises CUDA, or raises
 
 
 def desc(out_features: int, in_features: int, n: int, m: int) -> sbl_layer_desc:
@@ -419,9 +421,10 @@ def _ld(t: Optional[torch.Tensor]) -> int:
     """Row stride in elements of a matrix whose rows are contiguous."""
     if t is None:
         return 0
-    if t.dim() != 2 or t.stride(1) != 1:
+    s = t.stride()
+    if len(s) != 2 or s[1] != 1:
         raise ValueError("a 2-D tensor with contiguous rows is needed")
-    return t.stride(0) if t.size(0) > 1 else t.size(1)
+    return s[0] if t.shape[0] > 1 else t.shape[1]
 
 
 def _fp32(t: Optional[torch.Tensor]) -> int:

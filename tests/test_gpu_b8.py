@@ -394,7 +394,14 @@ def test_rmsnorm(typ, t, k, gains, residual):
     s, s0 = (torch.empty(t, dtype=torch.float32, device="cuda") for _ in range(2))
     sbl.sbl_quantize_act_rmsnorm_checkpoint(d, x, g, eps, q, s, x8)
     sbl.sbl_quantize_act_rmsnorm(x, t, k, g, eps, q0, s0)
-    assert torch.equal(q, q0) and torch.equal(s, s0)  # the forward itself is unchanged
+    # the forward's scales are the other entry point's; its codes are those of the factor 127 * (1 / a), which the
+    # quantiser's definition puts within one of the other's
+    assert torch.equal(s, s0) and int((q.int() - q0.int()).abs().max()) <= 1
+    rn = torch.from_numpy(1 / np.sqrt((xv * xv).sum(1, keepdims=True) / k + eps)).float()
+    un = torch.from_numpy(xv).float() * rn
+    un = un * torch.from_numpy(gv).float() if gains else un
+    an = un.abs().amax(1, keepdim=True)
+    assert torch.equal(q.cpu(), torch.round(un * (an.reciprocal() * 127)).to(torch.int8))
     check_stored(x8, k, typ, *ref.quantize(xv, typ))
     dx = torch.empty((t, k), dtype=torch.bfloat16, device="cuda")
     dg = torch.full((k + 4,), 6.0, dtype=torch.float32, device="cuda")
