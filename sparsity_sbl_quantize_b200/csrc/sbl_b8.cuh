@@ -75,8 +75,9 @@ __global__ void __launch_bounds__(256) b8_quantize_rows_kernel(B8RowArgs a)
                 uint32_t q[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    q[h] = b8_encode4<TYPE>(b8_scaled(v[i][h].x, inv), b8_scaled(v[i][h].y, inv),
-                                            b8_scaled(v[i][h].z, inv), b8_scaled(v[i][h].w, inv));
+                    q[h] = inv == 0.0f ? 0u
+                                       : b8_encode4<TYPE>(__fmul_rn(v[i][h].x, inv), __fmul_rn(v[i][h].y, inv),
+                                                          __fmul_rn(v[i][h].z, inv), __fmul_rn(v[i][h].w, inv));
                 *reinterpret_cast<uint2 *>(a.codes + row * a.ldc + c0 + 256 * i) = make_uint2(q[0], q[1]);
             }
             word |= byte << (8 * (2 * i + half));
@@ -126,7 +127,8 @@ __global__ void __launch_bounds__(256) b8_dequantize_kernel(B8ReadArgs a)
 
 // ------------------------------------------------------ tiles, transposed --
 // One CTA per 128 x 128 tile; thread (rg, cg) holds the 8 x 8 values at rows
-// 8 rg .., columns 8 cg .. in fp32 or packed bf16, so a row block is the 16
+// 8 rg .., columns 8 cg .. as they were read (decoded anew where needed: the
+// registers that this frees hold more loads in flight), so a row block is the 16
 // lanes of a half warp, a column block is 16 threads of one cg, and a
 // thread's column of eight is eight consecutive bytes of the transposed row.
 // Both orders come from one read of X; the transposed bytes pass through a
@@ -154,64 +156,83 @@ struct B8TileArgs {
 };
 
 template <int TYPE, int SRC, int SRC_TYPE, bool TILES>
-__global__ void __launch_bounds__(256) b8_tile_kernel(B8TileArgs a)
+__global__ void __launch_bounds__(256, SRC == kSrcF32 ? 2 : 4) b8_tile_kernel(B8TileArgs a)
 {
     __shared__ __align__(16) uint8_t tile[128 * 128];
-    __shared__ uint32_t colmax[16][128];
+    // a thread row's column maxima: two bf16 magnitudes a word, or fp32 bits
+    constexpr int kMaxWords = SRC == kSrcBf16 ? 64 : 128;
+    __shared__ __align__(16) uint32_t colmax[16][kMaxWords];
     __shared__ uint32_t wmax[8];
-    __shared__ uint8_t rbyte[128], cbyte[128];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ __align__(16) uint8_t rbyte[128], cbyte[128];
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31;
     const int rg = tid >> 4, cg = tid & 15;
     const int tr = static_cast<int>(blockIdx.x) / a.tiles_c;
     const int r0 = tr * 128, c0 = (static_cast<int>(blockIdx.x) - tr * a.tiles_c) * 128;
     const int col = c0 + 8 * cg;
     const bool col_ok = col < a.cols;
+    const int row = r0 + 8 * rg;  // the thread's first row
 
-    float v[8][8];
+    // the thread's values as they were read
+    uint4 q[SRC == kSrcBf16 ? 8 : 1];
+    float4 f[SRC == kSrcF32 ? 8 : 1][2];
+    uint2 b[SRC == kSrcB8 ? 8 : 1];
+    uint32_t bs[SRC == kSrcB8 ? 8 : 1];  // row scale bytes
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int row = r0 + 8 * rg + i;
-        const bool ok = col_ok && row < a.rows;
+        const bool ok = col_ok && row + i < a.rows;
+        const int64_t at = static_cast<int64_t>(row + i) * a.ldx + col;
         if constexpr (SRC == kSrcBf16) {
-            const uint4 q = ok ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.X) + row * a.ldx + col))
-                               : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[i][2 * j] = bf16_lo(w[j]), v[i][2 * j + 1] = bf16_hi(w[j]);
+            q[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.X) + at)) : make_uint4(0u, 0u, 0u, 0u);
         } else if constexpr (SRC == kSrcF32) {
-            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.X) + row * a.ldx + col);
+            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.X) + at);
             const float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const float4 x = ok ? __ldg(p) : z, y = ok ? __ldg(p + 1) : z;
-            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-            v[i][4] = y.x, v[i][5] = y.y, v[i][6] = y.z, v[i][7] = y.w;
+            f[i][0] = ok ? __ldg(p) : z;
+            f[i][1] = ok ? __ldg(p + 1) : z;
         } else {
-            const uint2 q = ok ? __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.X) + row * a.ldx + col))
-                               : make_uint2(0u, 0u);
             const int blk = c0 >> 7;
-            const uint32_t byte = ok ? __ldg(reinterpret_cast<const uint8_t *>(a.xs + b8_word_index(blk >> 2, a.xrp, row)) + (blk & 3)) : 127u;
-            const float s = b8_scale(byte);
-            float lo[4], hi[4];
-            b8_decode4<SRC_TYPE>(q.x, lo);
-            b8_decode4<SRC_TYPE>(q.y, hi);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[i][j] = __fmul_rn(lo[j], s), v[i][4 + j] = __fmul_rn(hi[j], s);
+            b[i] = ok ? __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.X) + at)) : make_uint2(0u, 0u);
+            bs[i] = ok ? __ldg(reinterpret_cast<const uint8_t *>(a.xs + b8_word_index(blk >> 2, a.xrp, row + i)) + (blk & 3)) : 127u;
         }
     }
+    // element j of row i, the eight of row i
+    auto row_values = [&](int i, float(&v)[8]) {
+        if constexpr (SRC == kSrcBf16) {
+            const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[2 * j] = bf16_lo(w[j]), v[2 * j + 1] = bf16_hi(w[j]);
+        } else if constexpr (SRC == kSrcF32) {
+            v[0] = f[i][0].x, v[1] = f[i][0].y, v[2] = f[i][0].z, v[3] = f[i][0].w;
+            v[4] = f[i][1].x, v[5] = f[i][1].y, v[6] = f[i][1].z, v[7] = f[i][1].w;
+        } else {
+            const float s = b8_scale(bs[i]);
+            float lo[4], hi[4];
+            b8_decode4<SRC_TYPE>(b[i].x, lo);
+            b8_decode4<SRC_TYPE>(b[i].y, hi);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = __fmul_rn(lo[j], s), v[4 + j] = __fmul_rn(hi[j], s);
+        }
+    };
     auto mag = [](float x) { return __float_as_uint(x) & 0x7fffffffu; };
-    uint32_t rmax[8];  // this thread's row maxima, then the blocks'
+    auto row_max = [&](int i) {
+        if constexpr (SRC == kSrcBf16) {
+            return bf16x8_absmax(q[i]) << 16;
+        } else {
+            float v[8];
+            row_values(i, v);
+            uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, mag(v[i][j]));
-        rmax[i] = m;
-    }
+            for (int j = 0; j < 8; ++j) m = max(m, mag(v[j]));
+            return m;
+        }
+    };
+
+    // ------------------------------------------------------- block scales
     if constexpr (TILES) {
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, rmax[i]);
+        for (int i = 0; i < 8; ++i) m = max(m, row_max(i));
         m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0) wmax[tid >> 5] = m;
         __syncthreads();
@@ -224,59 +245,98 @@ __global__ void __launch_bounds__(256) b8_tile_kernel(B8TileArgs a)
         if (a.codes) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(rmax[i]));
+                const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(row_max(i)));
                 if (cg == 0) rbyte[8 * rg + i] = static_cast<uint8_t>(byte);
             }
         }
         if (a.codes_t) {
+            if constexpr (SRC == kSrcBf16) {
+                uint4 m = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t m = 0;
+                for (int i = 0; i < 8; ++i) {
+                    m.x = __vmaxu2(m.x, q[i].x & 0x7fff7fffu);
+                    m.y = __vmaxu2(m.y, q[i].y & 0x7fff7fffu);
+                    m.z = __vmaxu2(m.z, q[i].z & 0x7fff7fffu);
+                    m.w = __vmaxu2(m.w, q[i].w & 0x7fff7fffu);
+                }
+                *reinterpret_cast<uint4 *>(&colmax[rg][4 * cg]) = m;
+                __syncthreads();
+                if (tid < 64) {
+                    uint32_t w = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m = max(m, mag(v[i][j]));
-                colmax[rg][8 * cg + j] = m;
-            }
-            __syncthreads();
-            if (tid < 128) {
-                uint32_t m = 0;
+                    for (int i = 0; i < 16; ++i) w = __vmaxu2(w, colmax[i][tid]);
+                    cbyte[2 * tid] = static_cast<uint8_t>(b8_scale_byte<TYPE>(w << 16));
+                    cbyte[2 * tid + 1] = static_cast<uint8_t>(b8_scale_byte<TYPE>(w & 0xffff0000u));
+                }
+            } else {
+                uint32_t m[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < 16; ++i) m = max(m, colmax[i][tid]);
-                cbyte[tid] = static_cast<uint8_t>(b8_scale_byte<TYPE>(m));
+                for (int i = 0; i < 8; ++i) {
+                    float v[8];
+                    row_values(i, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) m[j] = max(m[j], mag(v[j]));
+                }
+                // the two halves apart, so that a quarter warp's 16-byte stores
+                // fall on different banks
+                *reinterpret_cast<uint4 *>(&colmax[rg][4 * cg]) = make_uint4(m[0], m[1], m[2], m[3]);
+                *reinterpret_cast<uint4 *>(&colmax[rg][(kMaxWords / 2 + 4 * cg) % kMaxWords]) = make_uint4(m[4], m[5], m[6], m[7]);
+                __syncthreads();
+                if (tid < 128) {
+                    uint32_t w = 0;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w = max(w, colmax[i][tid % kMaxWords]);
+                    cbyte[8 * ((tid & 63) >> 2) + 4 * (tid >> 6) + (tid & 3)] = static_cast<uint8_t>(b8_scale_byte<TYPE>(w));
+                }
             }
         }
     }
     __syncthreads();
 
+    // ----------------------------------------------------------- row codes
     if (a.codes) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int row = r0 + 8 * rg + i;
-            if (!col_ok || row >= a.rows) continue;
+            if (!col_ok || row + i >= a.rows) continue;
             const float inv = b8_inv_scale(rbyte[8 * rg + i]);
-            const uint32_t lo = b8_encode4<TYPE>(b8_scaled(v[i][0], inv), b8_scaled(v[i][1], inv), b8_scaled(v[i][2], inv), b8_scaled(v[i][3], inv));
-            const uint32_t hi = b8_encode4<TYPE>(b8_scaled(v[i][4], inv), b8_scaled(v[i][5], inv), b8_scaled(v[i][6], inv), b8_scaled(v[i][7], inv));
-            *reinterpret_cast<uint2 *>(a.codes + row * a.ldc + col) = make_uint2(lo, hi);
+            float v[8];
+            row_values(i, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], inv);
+            uint2 w = make_uint2(b8_encode4<TYPE>(v[0], v[1], v[2], v[3]), b8_encode4<TYPE>(v[4], v[5], v[6], v[7]));
+            if (inv == 0.0f) w = make_uint2(0u, 0u);  // the block is not finite
+            *reinterpret_cast<uint2 *>(a.codes + static_cast<int64_t>(row + i) * a.ldc + col) = w;
         }
         // the tile's column of scale bytes (padded rows: 127; a word's blocks
         // past the last column are filled by the last block's tile)
         if (tid < 128) {
-            const int64_t row = r0 + tid;
+            const int64_t srow = r0 + tid;
             const int blk = c0 >> 7, nblk = (a.cols + 127) >> 7;
-            uint8_t *p = reinterpret_cast<uint8_t *>(a.scales + b8_word_index(blk >> 2, a.rp, row));
-            p[blk & 3] = row < a.rows ? rbyte[tid] : 127;
+            uint8_t *p = reinterpret_cast<uint8_t *>(a.scales + b8_word_index(blk >> 2, a.rp, srow));
+            p[blk & 3] = srow < a.rows ? rbyte[tid] : 127;
             if (blk == nblk - 1)
-                for (int b = (blk & 3) + 1; b < 4; ++b) p[b] = 127;
+                for (int k = (blk & 3) + 1; k < 4; ++k) p[k] = 127;
         }
     }
+    // ---------------------------------------------------- transposed codes
     if (a.codes_t) {
         // eight bytes (rows 8 rg ..) of transposed row 8 cg + j, the 16-byte
-        // chunk rg / 2 at position (rg / 2) ^ (cg % 8)
+        // chunk rg / 2 at position (rg / 2) ^ (cg % 8): scaled and encoded
+        // four rows at a time, a column's four codes in one word
+        const uint2 cb = *reinterpret_cast<const uint2 *>(cbyte + 8 * cg);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float inv = b8_inv_scale(cbyte[8 * cg + j]);
-            const uint32_t lo = b8_encode4<TYPE>(b8_scaled(v[0][j], inv), b8_scaled(v[1][j], inv), b8_scaled(v[2][j], inv), b8_scaled(v[3][j], inv));
-            const uint32_t hi = b8_encode4<TYPE>(b8_scaled(v[4][j], inv), b8_scaled(v[5][j], inv), b8_scaled(v[6][j], inv), b8_scaled(v[7][j], inv));
-            *reinterpret_cast<uint2 *>(tile + (8 * cg + j) * 128 + (((rg >> 1) ^ (cg & 7)) << 4) + 8 * (rg & 1)) = make_uint2(lo, hi);
+        for (int h = 0; h < 2; ++h) {
+            float v[4][8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) row_values(4 * h + i, v[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float inv = b8_inv_scale(((j < 4 ? cb.x : cb.y) >> (8 * (j & 3))) & 0xffu);
+                uint32_t w = b8_encode4<TYPE>(__fmul_rn(v[0][j], inv), __fmul_rn(v[1][j], inv), __fmul_rn(v[2][j], inv),
+                                              __fmul_rn(v[3][j], inv));
+                if (inv == 0.0f) w = 0u;
+                *reinterpret_cast<uint32_t *>(tile + (8 * cg + j) * 128 + (((rg >> 1) ^ (cg & 7)) << 4) + 8 * (rg & 1) + 4 * h) = w;
+            }
         }
         __syncthreads();
         // rows past the last are zero codes, so whole 16-byte chunks are
@@ -285,7 +345,7 @@ __global__ void __launch_bounds__(256) b8_tile_kernel(B8TileArgs a)
         for (int p = 0; p < 4; ++p) {
             const int k = p * 256 + tid;
             const int tc = k >> 3, ch = k & 7;
-            const int trow = c0 + tc;
+            const int64_t trow = c0 + tc;
             if (trow < a.cols && r0 + 16 * ch < a.ldt)
                 *reinterpret_cast<uint4 *>(a.codes_t + trow * a.ldt + r0 + 16 * ch) =
                     *reinterpret_cast<const uint4 *>(tile + tc * 128 + ((ch ^ ((tc >> 3) & 7)) << 4));
@@ -296,7 +356,7 @@ __global__ void __launch_bounds__(256) b8_tile_kernel(B8TileArgs a)
             uint8_t *p = reinterpret_cast<uint8_t *>(a.scales_t + b8_word_index(blk >> 2, a.rpt, trow));
             p[blk & 3] = trow < a.cols ? cbyte[tid] : 127;
             if (blk == nblk - 1)
-                for (int b = (blk & 3) + 1; b < 4; ++b) p[b] = 127;
+                for (int k = (blk & 3) + 1; k < 4; ++k) p[k] = 127;
         }
     }
 }

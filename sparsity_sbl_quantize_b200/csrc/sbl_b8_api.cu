@@ -472,20 +472,22 @@ static sbl_status norm_checkpoint(const uint16_t *X, int32_t T, int32_t K, const
     return SBL_ERR_SHAPE;
 }
 
-// Threads that share a row in the backward: at most four 8-element chunks
-// each (eight for the longest rows).
+// Threads that share a row in the backward: two 8-element chunks each (more
+// for rows longer than 1024 threads hold so).
 static int norm_row_threads(int32_t K)
 {
     int rt = 32;
-    while (rt < 1024 && rt * 4 < K / 8) rt *= 2;
+    while (rt < 1024 && rt * 2 < K / 8) rt *= 2;
     return rt;
 }
 
+// About 1024 threads an SM, each keeping its columns' part of the gains'
+// gradient while it goes through the rows.
 static int64_t norm_grid(int32_t T, int32_t K, int num_sms)
 {
     const int rt = norm_row_threads(K);
-    const int rows = rt >= 256 ? 1 : 256 / rt;
-    return std::min<int64_t>({(static_cast<int64_t>(T) + rows - 1) / rows, 2ll * num_sms, kNormPartials});
+    const int rows = rt >= 256 ? 1 : 256 / rt, block = std::max(rt, 256);
+    return std::min<int64_t>({(static_cast<int64_t>(T) + rows - 1) / rows, 1024ll / block * num_sms, kNormPartials});
 }
 
 template <int TYPE>
@@ -494,13 +496,13 @@ static sbl_status norm_backward(const NormBwdArgs &a, int64_t grid, cudaStream_t
     const int rt = norm_row_threads(a.K);
     const size_t smem = rt < 256 && a.partial ? static_cast<size_t>(a.K) * 4 : 0;
     switch (rt) {
-    case 32: return launch(norm_backward_kernel<TYPE, 32, 4>, grid, 256, smem, stream, a);
-    case 64: return launch(norm_backward_kernel<TYPE, 64, 4>, grid, 256, smem, stream, a);
-    case 128: return launch(norm_backward_kernel<TYPE, 128, 4>, grid, 256, smem, stream, a);
-    case 256: return launch(norm_backward_kernel<TYPE, 256, 4>, grid, 256, smem, stream, a);
-    case 512: return launch(norm_backward_kernel<TYPE, 512, 4>, grid, 512, smem, stream, a);
+    case 32: return launch(norm_backward_kernel<TYPE, 32, 2>, grid, 256, smem, stream, a);
+    case 64: return launch(norm_backward_kernel<TYPE, 64, 2>, grid, 256, smem, stream, a);
+    case 128: return launch(norm_backward_kernel<TYPE, 128, 2>, grid, 256, smem, stream, a);
+    case 256: return launch(norm_backward_kernel<TYPE, 256, 2>, grid, 256, smem, stream, a);
+    case 512: return launch(norm_backward_kernel<TYPE, 512, 2>, grid, 512, smem, stream, a);
     default:
-        return a.K <= 1024 * 4 * 8 ? launch(norm_backward_kernel<TYPE, 1024, 4>, grid, 1024, smem, stream, a)
+        return a.K <= 1024 * 2 * 8 ? launch(norm_backward_kernel<TYPE, 1024, 2>, grid, 1024, smem, stream, a)
                                    : launch(norm_backward_kernel<TYPE, 1024, 8>, grid, 1024, smem, stream, a);
     }
 }
@@ -850,7 +852,7 @@ sbl_status sbl_rmsnorm_backward(const sbl_b8_desc *desc, const sbl_b8 *x8, const
     default: st = norm_backward<kB8I8>(a, grid, s); break;
     }
     if (st != SBL_OK || !dg) return st;
-    return launch(norm_dgain_kernel, (K + 31) / 32, 256, 0, s, static_cast<const float *>(a.partial), static_cast<int32_t>(grid), K, dg);
+    return launch(norm_dgain_kernel, (K + 31) / 32, 1024, 0, s, static_cast<const float *>(a.partial), static_cast<int32_t>(grid), K, dg);
 }
 
 }  // extern "C"

@@ -78,9 +78,6 @@ __device__ __forceinline__ float b8_scale(uint32_t byte)
     return __uint_as_float(bits);
 }
 
-// x 2^-e of a block that may not be finite: 0 where inv is 0
-__device__ __forceinline__ float b8_scaled(float x, float inv) { return inv == 0.0f ? 0.0f : __fmul_rn(x, inv); }
-
 // Four codes of already scaled values, lowest address first.
 template <int TYPE>
 __device__ __forceinline__ uint32_t b8_encode4(float a, float b, float c, float d)
@@ -120,14 +117,16 @@ __device__ __forceinline__ uint32_t bf16x8_absmax(const uint4 &v)
     return max(m & 0xffffu, m >> 16);
 }
 
-// Eight bf16 values quantised with the factor inv.
+// Eight bf16 values quantised with the factor inv (0: a block that is not
+// finite, codes 0).
 template <int TYPE>
 __device__ __forceinline__ uint2 b8_encode_bf16x8(const uint4 &v, float inv)
 {
-    return make_uint2(b8_encode4<TYPE>(b8_scaled(bf16_lo(v.x), inv), b8_scaled(bf16_hi(v.x), inv),
-                                       b8_scaled(bf16_lo(v.y), inv), b8_scaled(bf16_hi(v.y), inv)),
-                      b8_encode4<TYPE>(b8_scaled(bf16_lo(v.z), inv), b8_scaled(bf16_hi(v.z), inv),
-                                       b8_scaled(bf16_lo(v.w), inv), b8_scaled(bf16_hi(v.w), inv)));
+    const uint2 w = make_uint2(b8_encode4<TYPE>(__fmul_rn(bf16_lo(v.x), inv), __fmul_rn(bf16_hi(v.x), inv),
+                                                __fmul_rn(bf16_lo(v.y), inv), __fmul_rn(bf16_hi(v.y), inv)),
+                               b8_encode4<TYPE>(__fmul_rn(bf16_lo(v.z), inv), __fmul_rn(bf16_hi(v.z), inv),
+                                                __fmul_rn(bf16_lo(v.w), inv), __fmul_rn(bf16_hi(v.w), inv)));
+    return inv == 0.0f ? make_uint2(0u, 0u) : w;
 }
 
 // max over the 16 lanes of a half warp

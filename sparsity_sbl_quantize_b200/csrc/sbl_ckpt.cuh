@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(256) glu_backward_kernel(GluBwdArgs a)
 // registers; the parts meet in shared memory (rows of one CTA, in order) and
 // then in norm_dgain_kernel (CTAs, in order), so the result is the same every
 // time.
-constexpr int kNormPartials = 512;  // most CTAs that leave a partial dgain
+constexpr int kNormPartials = 640;  // most CTAs that leave a partial dgain
 
 struct NormBwdArgs {
     const uint8_t *xc;
@@ -242,17 +242,18 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256) norm_backward_kernel(Norm
         const int64_t row = base + sub;
         const bool active = row < a.T;
         float x[NC][8];
-        uint4 du[NC];
+        uint4 du[NC], dr[NC];
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
             const int ci = lt + j * RT;
-            du[j] = make_uint4(0u, 0u, 0u, 0u);
+            du[j] = dr[j] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[j][k] = 0.0f;
             if (active && ci < chunks) {
                 const uint2 q = __ldg(reinterpret_cast<const uint2 *>(a.xc + row * a.ldc) + ci);
                 du[j] = __ldg(reinterpret_cast<const uint4 *>(a.dU + row * a.K) + ci);
+                if (a.dR) dr[j] = *(reinterpret_cast<const uint4 *>(a.dR + row * a.K) + ci);  // dR may be dX
                 const int blk = ci >> 4;
                 const uint32_t byte =
                     __ldg(reinterpret_cast<const uint8_t *>(a.xs + b8_word_index(blk >> 2, a.rp, row)) + (blk & 3));
@@ -281,9 +282,10 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256) norm_backward_kernel(Norm
             s2 += __shfl_xor_sync(0xffffffffu, s2, off);
         }
         if constexpr (W > 1) {
-            // two buffers in turn: one barrier a step suffices
+            // two buffers in turn: one barrier (of the row's threads) a step
+            // suffices
             if ((lt & 31) == 0) red[parity][sub][lt >> 5] = make_float2(s1, s2);
-            __syncthreads();
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "n"(RT) : "memory");
             s1 = s2 = 0.0f;
 #pragma unroll
             for (int w = 0; w < W; ++w) {
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256) norm_backward_kernel(Norm
             for (int k = 0; k < 8; ++k) o[k] = r * d[k] - c * x[j][k];
             if (a.dR) {
                 float e[8];
-                unpack_bf16x8(*(reinterpret_cast<const uint4 *>(a.dR + row * a.K) + ci), e);  // dR may be dX
+                unpack_bf16x8(dr[j], e);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) o[k] += e[k];
             }
@@ -348,23 +350,27 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256) norm_backward_kernel(Norm
     }
 }
 
-// dgain[k] = the sum of n partial rows, in 8 interleaved parts joined in order.
-__global__ void __launch_bounds__(256) norm_dgain_kernel(const float *__restrict__ partial, int32_t n, int32_t K,
-                                                         float *__restrict__ dgain)
+// dgain[k] = the sum of n partial rows, in 32 interleaved parts (a warp each)
+// joined in order.
+__global__ void __launch_bounds__(1024) norm_dgain_kernel(const float *__restrict__ partial, int32_t n, int32_t K,
+                                                          float *__restrict__ dgain)
 {
-    __shared__ float sh[8][32];
+    __shared__ float sh[32][33];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
     const int k = blockIdx.x * 32 + lane;
     float s = 0.0f;
-    if (k < K)
-        for (int i = part; i < n; i += 8) s += partial[static_cast<int64_t>(i) * K + k];
+    if (k < K) {
+#pragma unroll 4
+        for (int i = part; i < n; i += 32) s += partial[static_cast<int64_t>(i) * K + k];
+    }
     sh[part][lane] = s;
     __syncthreads();
     if (part == 0 && k < K) {
+        s = sh[0][lane];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += sh[i][lane];
+        for (int i = 1; i < 32; ++i) s += sh[i][lane];
         dgain[k] = s;
     }
 }
