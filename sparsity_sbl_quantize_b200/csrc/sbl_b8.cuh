@@ -19,6 +19,7 @@ struct B8RowArgs {
     uint32_t *scales;
     int64_t rp;         // rows padded to 128
     int32_t words;      // scale words per row
+    int32_t per_warp;   // of which a warp takes so many
 };
 
 template <int TYPE, int SRC>
@@ -29,62 +30,64 @@ __global__ void __launch_bounds__(256) b8_quantize_rows_kernel(B8RowArgs a)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, half = lane >> 4;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t row = unit / a.words;
-    const int w = static_cast<int>(unit - row * a.words);
-    if (row >= a.rp) return;
-    if (row >= a.rows) {
-        if (lane == 0) a.scales[b8_word_index(w, a.rp, row)] = kB8PadWord;
+    const B8Walk u = b8_walk(a.words, a.per_warp);
+    if (u.row >= a.rp) return;
+    uint32_t *scales = a.scales + b8_word_index(0, a.rp, u.row);
+    if (u.row >= a.rows) {
+        if (lane == 0)
+            for (int w = u.w0; w < u.w1; ++w) scales[w * a.rp] = kB8PadWord;
         return;
     }
-    uint32_t word = 0;
-    const int64_t c0 = static_cast<int64_t>(w) * 512 + 128 * half + 8 * (lane & 15);
-    if constexpr (SRC == kSrcBf16) {
-        uint4 v[2];
-        const uint16_t *x = static_cast<const uint16_t *>(a.X) + row * a.ldx;
+    const int l0 = 128 * half + 8 * (lane & 15);
+    uint8_t *codes = a.codes + u.row * a.ldc;
+    for (int w = u.w0; w < u.w1; ++w) {
+        uint32_t word = 0;
+        const int c0 = 512 * w + l0;
+        if constexpr (SRC == kSrcBf16) {
+            uint4 v[2];
+            const uint16_t *x = static_cast<const uint16_t *>(a.X) + u.row * a.ldx;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            v[i] = c0 + 256 * i < a.cols ? __ldg(reinterpret_cast<const uint4 *>(x + c0 + 256 * i)) : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 2; ++i)
+                v[i] = c0 + 256 * i < a.cols ? __ldg(reinterpret_cast<const uint4 *>(x + c0 + 256 * i)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(bf16x8_absmax(v[i])) << 16);
-            if (c0 + 256 * i < a.cols)
-                *reinterpret_cast<uint2 *>(a.codes + row * a.ldc + c0 + 256 * i) = b8_encode_bf16x8<TYPE>(v[i], b8_inv_scale(byte));
-            word |= byte << (8 * (2 * i + half));
-        }
-    } else {
-        float4 v[2][2];
-        const float *x = static_cast<const float *>(a.X) + row * a.ldx;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                v[i][h] = c0 + 256 * i < a.cols ? __ldg(reinterpret_cast<const float4 *>(x + c0 + 256 * i) + h)
-                                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                m = max(m, max(max(__float_as_uint(v[i][h].x) & 0x7fffffffu, __float_as_uint(v[i][h].y) & 0x7fffffffu),
-                               max(__float_as_uint(v[i][h].z) & 0x7fffffffu, __float_as_uint(v[i][h].w) & 0x7fffffffu)));
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(bf16x8_absmax(v[i])) << 16);
+                const uint2 q = b8_encode_bf16x8<TYPE>(v[i], b8_inv_scale(byte));
+                if (c0 + 256 * i < a.cols) *reinterpret_cast<uint2 *>(codes + c0 + 256 * i) = q;
+                word |= byte << (8 * (2 * i + half));
             }
-            const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(m));
-            const float inv = b8_inv_scale(byte);
-            if (c0 + 256 * i < a.cols) {
+        } else {
+            float4 v[2][2];
+            const float *x = static_cast<const float *>(a.X) + u.row * a.ldx;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    v[i][h] = c0 + 256 * i < a.cols ? __ldg(reinterpret_cast<const float4 *>(x + c0 + 256 * i) + h)
+                                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    m = max(m, max(max(__float_as_uint(v[i][h].x) & 0x7fffffffu, __float_as_uint(v[i][h].y) & 0x7fffffffu),
+                                   max(__float_as_uint(v[i][h].z) & 0x7fffffffu, __float_as_uint(v[i][h].w) & 0x7fffffffu)));
+                }
+                const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(m));
+                const float inv = b8_inv_scale(byte);
                 uint32_t q[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     q[h] = inv == 0.0f ? 0u
                                        : b8_encode4<TYPE>(__fmul_rn(v[i][h].x, inv), __fmul_rn(v[i][h].y, inv),
                                                           __fmul_rn(v[i][h].z, inv), __fmul_rn(v[i][h].w, inv));
-                *reinterpret_cast<uint2 *>(a.codes + row * a.ldc + c0 + 256 * i) = make_uint2(q[0], q[1]);
+                if (c0 + 256 * i < a.cols) *reinterpret_cast<uint2 *>(codes + c0 + 256 * i) = make_uint2(q[0], q[1]);
+                word |= byte << (8 * (2 * i + half));
             }
-            word |= byte << (8 * (2 * i + half));
         }
+        word |= __shfl_xor_sync(0xffffffffu, word, 16);
+        if (lane == 0) scales[w * a.rp] = word;
     }
-    word |= __shfl_xor_sync(0xffffffffu, word, 16);
-    if (lane == 0) a.scales[b8_word_index(w, a.rp, row)] = word;
 }
 
 // Codes and scales back to bf16 (one rounding of code 2^e, exact unless the
@@ -94,7 +97,7 @@ struct B8ReadArgs {
     int64_t ldc;
     const uint32_t *scales;
     int64_t rp;
-    int32_t rows, cols, words;
+    int32_t rows, cols, words, per_warp;
     uint16_t *X;
     int64_t ldx;
 };
@@ -105,23 +108,21 @@ __global__ void __launch_bounds__(256) b8_dequantize_kernel(B8ReadArgs a)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, half = lane >> 4;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t row = unit / a.words;
-    const int w = static_cast<int>(unit - row * a.words);
-    if (row >= a.rows) return;
-    const int64_t c0 = static_cast<int64_t>(w) * 512 + 128 * half + 8 * (lane & 15);
-    const uint32_t word = __ldg(a.scales + b8_word_index(w, a.rp, row));
+    const B8Walk u = b8_walk(a.words, a.per_warp);
+    if (u.row >= a.rows) return;
+    const uint32_t *scales = a.scales + b8_word_index(0, a.rp, u.row);
+    const int l0 = 128 * half + 8 * (lane & 15);
+    for (int w = u.w0; w < u.w1; ++w) {
+        const int c0 = 512 * w + l0;
+        const uint32_t word = __ldg(scales + w * a.rp);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (c0 + 256 * i >= a.cols) continue;
-        const uint2 q = __ldg(reinterpret_cast<const uint2 *>(a.codes + row * a.ldc + c0 + 256 * i));
-        const float s = b8_scale((word >> (8 * (2 * i + half))) & 0xffu);
-        float lo[4], hi[4];
-        b8_decode4<TYPE>(q.x, lo);
-        b8_decode4<TYPE>(q.y, hi);
-        *reinterpret_cast<uint4 *>(a.X + row * a.ldx + c0 + 256 * i) =
-            make_uint4(pack_bf16(__fmul_rn(lo[0], s), __fmul_rn(lo[1], s)), pack_bf16(__fmul_rn(lo[2], s), __fmul_rn(lo[3], s)),
-                       pack_bf16(__fmul_rn(hi[0], s), __fmul_rn(hi[1], s)), pack_bf16(__fmul_rn(hi[2], s), __fmul_rn(hi[3], s)));
+        for (int i = 0; i < 2; ++i) {
+            if (c0 + 256 * i >= a.cols) continue;
+            const uint2 q = __ldg(reinterpret_cast<const uint2 *>(a.codes + u.row * a.ldc + c0 + 256 * i));
+            float v[8];
+            b8_load8<TYPE>(q, b8_scale((word >> (8 * (2 * i + half))) & 0xffu), v);
+            *reinterpret_cast<uint4 *>(a.X + u.row * a.ldx + c0 + 256 * i) = pack_bf16x8(v);
+        }
     }
 }
 
@@ -178,7 +179,14 @@ __global__ void __launch_bounds__(256, SRC == kSrcF32 ? 2 : 4) b8_tile_kernel(B8
     uint4 q[SRC == kSrcBf16 ? 8 : 1];
     float4 f[SRC == kSrcF32 ? 8 : 1][2];
     uint2 b[SRC == kSrcB8 ? 8 : 1];
-    uint32_t bs[SRC == kSrcB8 ? 8 : 1];  // row scale bytes
+    __shared__ __align__(16) float rscale[SRC == kSrcB8 ? 128 : 4];  // 2^e of the source's rows
+    if constexpr (SRC == kSrcB8) {
+        const int blk = c0 >> 7;
+        if (tid < 128)
+            rscale[tid] = r0 + tid < a.rows
+                              ? b8_scale(__ldg(reinterpret_cast<const uint8_t *>(a.xs + b8_word_index(blk >> 2, a.xrp, r0 + tid)) + (blk & 3)))
+                              : 1.0f;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const bool ok = col_ok && row + i < a.rows;
@@ -191,11 +199,10 @@ __global__ void __launch_bounds__(256, SRC == kSrcF32 ? 2 : 4) b8_tile_kernel(B8
             f[i][0] = ok ? __ldg(p) : z;
             f[i][1] = ok ? __ldg(p + 1) : z;
         } else {
-            const int blk = c0 >> 7;
             b[i] = ok ? __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.X) + at)) : make_uint2(0u, 0u);
-            bs[i] = ok ? __ldg(reinterpret_cast<const uint8_t *>(a.xs + b8_word_index(blk >> 2, a.xrp, row + i)) + (blk & 3)) : 127u;
         }
     }
+    if constexpr (SRC == kSrcB8) __syncthreads();
     // element j of row i, the eight of row i
     auto row_values = [&](int i, float(&v)[8]) {
         if constexpr (SRC == kSrcBf16) {
@@ -206,12 +213,7 @@ __global__ void __launch_bounds__(256, SRC == kSrcF32 ? 2 : 4) b8_tile_kernel(B8
             v[0] = f[i][0].x, v[1] = f[i][0].y, v[2] = f[i][0].z, v[3] = f[i][0].w;
             v[4] = f[i][1].x, v[5] = f[i][1].y, v[6] = f[i][1].z, v[7] = f[i][1].w;
         } else {
-            const float s = b8_scale(bs[i]);
-            float lo[4], hi[4];
-            b8_decode4<SRC_TYPE>(b[i].x, lo);
-            b8_decode4<SRC_TYPE>(b[i].y, hi);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = __fmul_rn(lo[j], s), v[4 + j] = __fmul_rn(hi[j], s);
+            b8_load8<SRC_TYPE>(b[i], rscale[8 * rg + i], v);
         }
     };
     auto mag = [](float x) { return __float_as_uint(x) & 0x7fffffffu; };

@@ -61,12 +61,12 @@ static sbl_status b8_device(HostDevice *hd)
 // Launch with programmatic dependent launch: every kernel here waits for the
 // one before it (griddepcontrol.wait) before it touches global memory.
 template <typename... P, typename... A>
-static sbl_status launch(void (*kernel)(P...), int64_t grid, int block, size_t smem, cudaStream_t stream, A... args)
+static sbl_status launch2(void (*kernel)(P...), int64_t grid, int64_t grid_y, int block, size_t smem, cudaStream_t stream, A... args)
 {
-    if (grid > 0x7fffffffll) return SBL_ERR_SHAPE;
+    if (grid > 0x7fffffffll || grid_y > 65535) return SBL_ERR_SHAPE;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>(grid_y));
     cfg.blockDim = dim3(static_cast<unsigned>(block));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -77,6 +77,27 @@ static sbl_status launch(void (*kernel)(P...), int64_t grid, int block, size_t s
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return SBL_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SBL_OK : SBL_ERR_CUDA;
+}
+
+template <typename... P, typename... A>
+static sbl_status launch(void (*kernel)(P...), int64_t grid, int block, size_t smem, cudaStream_t stream, A... args)
+{
+    return launch2(kernel, grid, 1, block, smem, stream, args...);
+}
+
+// Scale words (512 columns) a warp of the element-wise kernels takes: one
+// while the rows alone do not fill the device twice over, four after that.
+static int32_t words_per_warp(int64_t rows, int32_t words, int num_sms)
+{
+    const int64_t fit = rows * words / (2 * 64ll * num_sms);
+    return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({4, fit, words})));
+}
+
+template <typename Args>
+static sbl_status launch_walk(const HostDevice &hd, void (*kernel)(Args), int64_t rows, Args a, cudaStream_t stream)
+{
+    a.per_warp = words_per_warp(rows, a.words, hd.num_sms);
+    return launch2(kernel, (rows + 7) / 8, (a.words + a.per_warp - 1) / a.per_warp, 256, 0, stream, a);
 }
 
 // ------------------------------------------------------------ descriptors --
@@ -116,7 +137,7 @@ static sbl_status check_strided(const void *p, int64_t ld, int64_t cols, int ele
 
 // -------------------------------------------------------------- quantiser --
 template <int TYPE, int SRC>
-static sbl_status quantize_rows(const sbl_b8_desc *d, const void *X, int64_t ldx, const sbl_b8 *out, cudaStream_t stream)
+static sbl_status quantize_rows(const HostDevice &hd, const sbl_b8_desc *d, const void *X, int64_t ldx, const sbl_b8 *out, cudaStream_t stream)
 {
     B8RowArgs a;
     memset(&a, 0, sizeof(a));
@@ -129,7 +150,7 @@ static sbl_status quantize_rows(const sbl_b8_desc *d, const void *X, int64_t ldx
     a.scales = scale_words(out);
     a.rp = b8_rp(d->rows);
     a.words = b8_words(d->cols);
-    return launch(b8_quantize_rows_kernel<TYPE, SRC>, (a.rp * a.words + 7) / 8, 256, 0, stream, a);
+    return launch_walk(hd, b8_quantize_rows_kernel<TYPE, SRC>, a.rp, a, stream);
 }
 
 template <int TYPE, int SRC, int SRC_TYPE, bool TILES>
@@ -161,11 +182,11 @@ static sbl_status quantize_tiles(const sbl_b8_desc *d, const void *X, int64_t ld
 }
 
 template <int TYPE>
-static sbl_status quantize_type(const sbl_b8_desc *d, const void *X, bool fp32, int64_t ldx, bool tiles, const sbl_b8 *out,
+static sbl_status quantize_type(const HostDevice &hd, const sbl_b8_desc *d, const void *X, bool fp32, int64_t ldx, bool tiles, const sbl_b8 *out,
                                 const sbl_b8 *out_t, cudaStream_t stream)
 {
     if (!tiles && !out_t)
-        return fp32 ? quantize_rows<TYPE, kSrcF32>(d, X, ldx, out, stream) : quantize_rows<TYPE, kSrcBf16>(d, X, ldx, out, stream);
+        return fp32 ? quantize_rows<TYPE, kSrcF32>(hd, d, X, ldx, out, stream) : quantize_rows<TYPE, kSrcBf16>(hd, d, X, ldx, out, stream);
     if (tiles)
         return fp32 ? quantize_tiles<TYPE, kSrcF32, 0, true>(d, X, ldx, nullptr, out, out_t, stream)
                     : quantize_tiles<TYPE, kSrcBf16, 0, true>(d, X, ldx, nullptr, out, out_t, stream);
@@ -173,13 +194,13 @@ static sbl_status quantize_type(const sbl_b8_desc *d, const void *X, bool fp32, 
                 : quantize_tiles<TYPE, kSrcBf16, 0, false>(d, X, ldx, nullptr, out, out_t, stream);
 }
 
-static sbl_status quantize(const sbl_b8_desc *d, const void *X, bool fp32, int64_t ldx, bool tiles, const sbl_b8 *out,
+static sbl_status quantize(const HostDevice &hd, const sbl_b8_desc *d, const void *X, bool fp32, int64_t ldx, bool tiles, const sbl_b8 *out,
                            const sbl_b8 *out_t, cudaStream_t stream)
 {
     switch (d->type) {
-    case SBL_B8_E4M3: return quantize_type<kB8E4M3>(d, X, fp32, ldx, tiles, out, out_t, stream);
-    case SBL_B8_E5M2: return quantize_type<kB8E5M2>(d, X, fp32, ldx, tiles, out, out_t, stream);
-    default: return quantize_type<kB8I8>(d, X, fp32, ldx, tiles, out, out_t, stream);
+    case SBL_B8_E4M3: return quantize_type<kB8E4M3>(hd, d, X, fp32, ldx, tiles, out, out_t, stream);
+    case SBL_B8_E5M2: return quantize_type<kB8E5M2>(hd, d, X, fp32, ldx, tiles, out, out_t, stream);
+    default: return quantize_type<kB8I8>(hd, d, X, fp32, ldx, tiles, out, out_t, stream);
     }
 }
 
@@ -496,32 +517,31 @@ static sbl_status norm_backward(const NormBwdArgs &a, int64_t grid, cudaStream_t
     const int rt = norm_row_threads(a.K);
     const size_t smem = rt < 256 && a.partial ? static_cast<size_t>(a.K) * 4 : 0;
     switch (rt) {
-    case 32: return launch(norm_backward_kernel<TYPE, 32, 2>, grid, 256, smem, stream, a);
-    case 64: return launch(norm_backward_kernel<TYPE, 64, 2>, grid, 256, smem, stream, a);
-    case 128: return launch(norm_backward_kernel<TYPE, 128, 2>, grid, 256, smem, stream, a);
-    case 256: return launch(norm_backward_kernel<TYPE, 256, 2>, grid, 256, smem, stream, a);
-    case 512: return launch(norm_backward_kernel<TYPE, 512, 2>, grid, 512, smem, stream, a);
+    case 32: return launch(norm_backward_kernel<TYPE, 32, 2, true>, grid, 256, smem, stream, a);
+    case 64: return launch(norm_backward_kernel<TYPE, 64, 2, true>, grid, 256, smem, stream, a);
+    case 128: return launch(norm_backward_kernel<TYPE, 128, 2, true>, grid, 256, smem, stream, a);
+    case 256: return launch(norm_backward_kernel<TYPE, 256, 2, true>, grid, 256, smem, stream, a);
+    case 512: return launch(norm_backward_kernel<TYPE, 512, 2, true>, grid, 512, smem, stream, a);
     default:
-        return a.K <= 1024 * 2 * 8 ? launch(norm_backward_kernel<TYPE, 1024, 2>, grid, 1024, smem, stream, a)
-                                   : launch(norm_backward_kernel<TYPE, 1024, 8>, grid, 1024, smem, stream, a);
+        return a.K <= 1024 * 2 * 8 ? launch(norm_backward_kernel<TYPE, 1024, 2, false>, grid, 1024, smem, stream, a)
+                                   : launch(norm_backward_kernel<TYPE, 1024, 8, false>, grid, 1024, smem, stream, a);
     }
 }
 
 // ------------------------------------------------------------- activation --
 template <int TYPE, int ACT>
-static sbl_status glu_forward(const GluFwdArgs &a, cudaStream_t stream)
+static sbl_status glu_forward(const HostDevice &hd, const GluFwdArgs &a, cudaStream_t stream)
 {
-    const int64_t grid = ((a.gc || a.uc ? a.rp : a.rows) * a.words + 7) / 8;
-    return a.U ? launch(glu_forward_kernel<TYPE, ACT, true>, grid, 256, 0, stream, a)
-               : launch(glu_forward_kernel<TYPE, ACT, false>, grid, 256, 0, stream, a);
+    const int64_t rows = a.gc || a.uc ? a.rp : a.rows;  // padded rows have scales to write
+    return a.U ? launch_walk(hd, glu_forward_kernel<TYPE, ACT, true>, rows, a, stream)
+               : launch_walk(hd, glu_forward_kernel<TYPE, ACT, false>, rows, a, stream);
 }
 
 template <int TYPE, int ACT>
-static sbl_status glu_backward(const GluBwdArgs &a, cudaStream_t stream)
+static sbl_status glu_backward(const HostDevice &hd, const GluBwdArgs &a, cudaStream_t stream)
 {
-    const int64_t grid = (static_cast<int64_t>(a.rows) * a.words + 7) / 8;
-    return a.uc ? launch(glu_backward_kernel<TYPE, ACT, true>, grid, 256, 0, stream, a)
-                : launch(glu_backward_kernel<TYPE, ACT, false>, grid, 256, 0, stream, a);
+    return a.uc ? launch_walk(hd, glu_backward_kernel<TYPE, ACT, true>, a.rows, a, stream)
+                : launch_walk(hd, glu_backward_kernel<TYPE, ACT, false>, a.rows, a, stream);
 }
 
 }  // namespace sbl
@@ -549,7 +569,7 @@ sbl_status sbl_b8_quantize(const sbl_b8_desc *desc, const void *X, int32_t x_is_
     if ((out && !b8_aligned(out)) || (out_t && !b8_aligned(out_t))) return SBL_ERR_ALIGNMENT;
     HostDevice hd;
     if ((st = b8_device(&hd)) != SBL_OK) return st;
-    return quantize(desc, X, x_is_fp32 != 0, ldx, blocks == SBL_B8_TILES, out, out_t, static_cast<cudaStream_t>(stream));
+    return quantize(hd, desc, X, x_is_fp32 != 0, ldx, blocks == SBL_B8_TILES, out, out_t, static_cast<cudaStream_t>(stream));
 }
 
 sbl_status sbl_b8_transpose(const sbl_b8_desc *desc, const sbl_b8 *in, int32_t type_t, const sbl_b8 *out_t, void *stream)
@@ -586,12 +606,11 @@ sbl_status sbl_b8_dequantize(const sbl_b8_desc *desc, const sbl_b8 *in, uint16_t
     a.words = b8_words(desc->cols);
     a.X = X;
     a.ldx = ldx;
-    const int64_t grid = (static_cast<int64_t>(a.rows) * a.words + 7) / 8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (desc->type) {
-    case SBL_B8_E4M3: return launch(b8_dequantize_kernel<kB8E4M3>, grid, 256, 0, s, a);
-    case SBL_B8_E5M2: return launch(b8_dequantize_kernel<kB8E5M2>, grid, 256, 0, s, a);
-    default: return launch(b8_dequantize_kernel<kB8I8>, grid, 256, 0, s, a);
+    case SBL_B8_E4M3: return launch_walk(hd, b8_dequantize_kernel<kB8E4M3>, a.rows, a, s);
+    case SBL_B8_E5M2: return launch_walk(hd, b8_dequantize_kernel<kB8E5M2>, a.rows, a, s);
+    default: return launch_walk(hd, b8_dequantize_kernel<kB8I8>, a.rows, a, s);
     }
 }
 
@@ -648,7 +667,7 @@ sbl_status sbl_b8_linear_forward(const sbl_b8_desc *w_desc, const sbl_b8 *w, con
         if (p.smem <= kB8SmemAll && static_cast<int64_t>(T) * p.max_blocks <= 64 && !(y_is_fp32 && p.max_blocks > kB8SegBlocks))
             return skinny(hd, p, w_desc, w, &xd, X, ldx, xq, Y, ldy, y_is_fp32 != 0, false, false, s);
     }
-    if ((st = quantize(&xd, X, false, ldx, false, xq, nullptr, s)) != SBL_OK) return st;
+    if ((st = quantize(hd, &xd, X, false, ldx, false, xq, nullptr, s)) != SBL_OK) return st;
     return gemm(hd, &xd, xq, w_desc, w, Y, ldy, y_is_fp32 != 0, false, true, s);
 }
 
@@ -687,7 +706,7 @@ sbl_status sbl_b8_linear_backward(const sbl_b8_desc *w_desc, const sbl_b8 *w_t, 
     const BackwardPlan p = backward_plan(O, K, T, g_type, x_type);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const sbl_b8 g = {ws + p.g_codes, ws + p.g_scales}, gt = {ws + p.gt_codes, ws + p.gt_scales}, xt = {ws + p.xt_codes, ws + p.xt_scales};
-    if ((st = quantize(&gd, dY, false, lddy, false, dX ? &g : nullptr, dW ? &gt : nullptr, s)) != SBL_OK) return st;
+    if ((st = quantize(hd, &gd, dY, false, lddy, false, dX ? &g : nullptr, dW ? &gt : nullptr, s)) != SBL_OK) return st;
     if (dX) {
         const sbl_b8_desc wt = {K, O, w_desc->type};
         if ((st = gemm(hd, &p.g, &g, &wt, w_t, dX, K, dx_is_fp32 != 0, false, false, s)) != SBL_OK) return st;
@@ -730,12 +749,12 @@ sbl_status sbl_glu_forward(const sbl_b8_desc *desc, sbl_activation act, const ui
     a.words = b8_words(desc->cols);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (desc->type * 2 + act) {
-    case SBL_B8_E4M3 * 2 + SBL_ACT_SILU: return glu_forward<kB8E4M3, kActSilu>(a, s);
-    case SBL_B8_E4M3 * 2 + SBL_ACT_RELU2: return glu_forward<kB8E4M3, kActRelu2>(a, s);
-    case SBL_B8_E5M2 * 2 + SBL_ACT_SILU: return glu_forward<kB8E5M2, kActSilu>(a, s);
-    case SBL_B8_E5M2 * 2 + SBL_ACT_RELU2: return glu_forward<kB8E5M2, kActRelu2>(a, s);
-    case SBL_B8_I8 * 2 + SBL_ACT_SILU: return glu_forward<kB8I8, kActSilu>(a, s);
-    default: return glu_forward<kB8I8, kActRelu2>(a, s);
+    case SBL_B8_E4M3 * 2 + SBL_ACT_SILU: return glu_forward<kB8E4M3, kActSilu>(hd, a, s);
+    case SBL_B8_E4M3 * 2 + SBL_ACT_RELU2: return glu_forward<kB8E4M3, kActRelu2>(hd, a, s);
+    case SBL_B8_E5M2 * 2 + SBL_ACT_SILU: return glu_forward<kB8E5M2, kActSilu>(hd, a, s);
+    case SBL_B8_E5M2 * 2 + SBL_ACT_RELU2: return glu_forward<kB8E5M2, kActRelu2>(hd, a, s);
+    case SBL_B8_I8 * 2 + SBL_ACT_SILU: return glu_forward<kB8I8, kActSilu>(hd, a, s);
+    default: return glu_forward<kB8I8, kActRelu2>(hd, a, s);
     }
 }
 
@@ -771,12 +790,12 @@ sbl_status sbl_glu_backward(const sbl_b8_desc *desc, sbl_activation act, const s
     a.words = b8_words(desc->cols);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (desc->type * 2 + act) {
-    case SBL_B8_E4M3 * 2 + SBL_ACT_SILU: return glu_backward<kB8E4M3, kActSilu>(a, s);
-    case SBL_B8_E4M3 * 2 + SBL_ACT_RELU2: return glu_backward<kB8E4M3, kActRelu2>(a, s);
-    case SBL_B8_E5M2 * 2 + SBL_ACT_SILU: return glu_backward<kB8E5M2, kActSilu>(a, s);
-    case SBL_B8_E5M2 * 2 + SBL_ACT_RELU2: return glu_backward<kB8E5M2, kActRelu2>(a, s);
-    case SBL_B8_I8 * 2 + SBL_ACT_SILU: return glu_backward<kB8I8, kActSilu>(a, s);
-    default: return glu_backward<kB8I8, kActRelu2>(a, s);
+    case SBL_B8_E4M3 * 2 + SBL_ACT_SILU: return glu_backward<kB8E4M3, kActSilu>(hd, a, s);
+    case SBL_B8_E4M3 * 2 + SBL_ACT_RELU2: return glu_backward<kB8E4M3, kActRelu2>(hd, a, s);
+    case SBL_B8_E5M2 * 2 + SBL_ACT_SILU: return glu_backward<kB8E5M2, kActSilu>(hd, a, s);
+    case SBL_B8_E5M2 * 2 + SBL_ACT_RELU2: return glu_backward<kB8E5M2, kActRelu2>(hd, a, s);
+    case SBL_B8_I8 * 2 + SBL_ACT_SILU: return glu_backward<kB8I8, kActSilu>(hd, a, s);
+    default: return glu_backward<kB8I8, kActRelu2>(hd, a, s);
     }
 }
 

@@ -129,6 +129,20 @@ __device__ __forceinline__ uint2 b8_encode_bf16x8(const uint4 &v, float inv)
     return inv == 0.0f ? make_uint2(0u, 0u) : w;
 }
 
+// How the element-wise kernels walk a matrix: warp v of a CTA takes row
+// 8 blockIdx.x + v and the scale words [w0, w1) of it (512 columns each); no
+// division, and a few words a warp amortise the row's addresses.
+struct B8Walk {
+    int64_t row;
+    int w0, w1;
+};
+
+__device__ __forceinline__ B8Walk b8_walk(int words, int per_warp)
+{
+    const int w0 = static_cast<int>(blockIdx.y) * per_warp;
+    return {static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5), w0, min(w0 + per_warp, words)};
+}
+
 // max over the 16 lanes of a half warp
 __device__ __forceinline__ uint32_t half_warp_max(uint32_t v)
 {
@@ -141,6 +155,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
 {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4 &q, float (&v)[8])
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8])
+{
+    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+
+// Eight codes of one block decoded with its scale s = 2^e.
+template <int TYPE>
+__device__ __forceinline__ void b8_load8(const uint2 &q, float s, float (&v)[8])
+{
+    float lo[4], hi[4];
+    b8_decode4<TYPE>(q.x, lo);
+    b8_decode4<TYPE>(q.y, hi);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __fmul_rn(lo[k], s), v[4 + k] = __fmul_rn(hi[k], s);
 }
 
 }  // namespace sbl

@@ -18,9 +18,24 @@ enum ActKind : int { kActSilu = 0, kActRelu2 = 1 };
 // act(g), and act'(g) beside it.  relu2(g) = max(g, 0)^2, relu2' = 2 max(g, 0).
 // silu(g) = g s, s = 1 / (1 + e^-g), silu' = s (1 + g (1 - s)), with
 // t = e^-|g| <= 1:  s = (g < 0 ? t : 1) / (1 + t),  1 - s = (g < 0 ? 1 : t) / (1 + t),
-// so that nothing overflows and far negative g keep their (tiny) values.
-// __expf is off by about |g| 2^-23 and __fdividef by 2^-22, far below the
-// bf16 results' half step of 2^-8.
+// so that nothing overflows and far negative g keep their (tiny) values: t is
+// the square of e^-|g|/2, which the flushing form of ex2 still holds.  t is off
+// by about |g| 2^-23 and the reciprocal by 2^-23, far below the bf16 results'
+// half step of 2^-8.
+__device__ __forceinline__ float exp_neg_abs(float g)
+{
+    float h;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(__fmul_rn(fabsf(g), -0.72134752f)));  // -log2(e) / 2
+    return __fmul_rn(h, h);
+}
+
+__device__ __forceinline__ float rcp_approx(float x)  // x in [1, 2]
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float g)
 {
@@ -28,8 +43,8 @@ __device__ __forceinline__ float act_value(float g)
         const float p = g < 0.0f ? 0.0f : g;  // a NaN stays one
         return p * p;
     } else {
-        const float t = __expf(-fabsf(g));
-        return g * __fdividef(g < 0.0f ? t : 1.0f, 1.0f + t);
+        const float t = exp_neg_abs(g);
+        return g * ((g < 0.0f ? t : 1.0f) * rcp_approx(1.0f + t));
     }
 }
 
@@ -39,26 +54,13 @@ __device__ __forceinline__ void act_value_grad(float g, float &a, float &da)
     if constexpr (ACT == kActRelu2) {
         const float p = g < 0.0f ? 0.0f : g;
         a = p * p;
-        da = 2.0f * p;
+        da = p + p;
     } else {
-        const float t = __expf(-fabsf(g));
-        const float inv = __fdividef(1.0f, 1.0f + t);
-        const float s = g < 0.0f ? t * inv : inv, rest = g < 0.0f ? inv : t * inv;
+        const float t = exp_neg_abs(g), inv = rcp_approx(1.0f + t), ti = t * inv;
+        const float s = g < 0.0f ? ti : inv, rest = g < 0.0f ? inv : ti;
         a = g * s;
         da = s * fmaf(g, rest, 1.0f);
     }
-}
-
-__device__ __forceinline__ void unpack_bf16x8(const uint4 &q, float (&v)[8])
-{
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
-}
-
-__device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8])
-{
-    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
 // h = act(g) u (u absent: h = act(g)), with the checkpoints of g and u.  The
@@ -73,7 +75,7 @@ struct GluFwdArgs {
     uint32_t *gs, *us;
     int64_t ldc;
     int64_t rp;
-    int32_t rows, cols, words;
+    int32_t rows, cols, words, per_warp;
 };
 
 template <int TYPE, int ACT, bool GATED>
@@ -82,58 +84,61 @@ __global__ void __launch_bounds__(256) glu_forward_kernel(GluFwdArgs a)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, half = lane >> 4;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t row = unit / a.words;
-    const int w = static_cast<int>(unit - row * a.words);
-    if (row >= a.rp) return;
-    const int64_t wi = b8_word_index(w, a.rp, row);
-    if (row >= a.rows) {
-        if (lane == 0) {
-            if (a.gc) a.gs[wi] = kB8PadWord;
-            if (GATED && a.uc) a.us[wi] = kB8PadWord;
-        }
+    const B8Walk wk = b8_walk(a.words, a.per_warp);
+    if (wk.row >= a.rp) return;
+    const int64_t wi = b8_word_index(0, a.rp, wk.row);
+    if (wk.row >= a.rows) {
+        if (lane == 0)
+            for (int w = wk.w0; w < wk.w1; ++w) {
+                if (a.gc) a.gs[wi + w * a.rp] = kB8PadWord;
+                if (GATED && a.uc) a.us[wi + w * a.rp] = kB8PadWord;
+            }
         return;
     }
-    const int64_t c0 = static_cast<int64_t>(w) * 512 + 128 * half + 8 * (lane & 15);
+    const int l0 = 128 * half + 8 * (lane & 15);
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    uint4 g[2], u[2];
+    const uint16_t *G = a.G + wk.row * a.ldg, *U = GATED ? a.U + wk.row * a.ldu : nullptr;
+    for (int w = wk.w0; w < wk.w1; ++w) {
+        const int c0 = 512 * w + l0;
+        uint4 g[2], u[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const bool ok = c0 + 256 * i < a.cols;
-        g[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(a.G + row * a.ldg + c0 + 256 * i)) : z;
-        u[i] = GATED && ok ? __ldg(reinterpret_cast<const uint4 *>(a.U + row * a.ldu + c0 + 256 * i)) : z;
-    }
-    uint32_t gw = 0, uw = 0;
+        for (int i = 0; i < 2; ++i) {
+            const bool ok = c0 + 256 * i < a.cols;
+            g[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(G + c0 + 256 * i)) : z;
+            if (GATED) u[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(U + c0 + 256 * i)) : z;
+        }
+        uint32_t gw = 0, uw = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t c = c0 + 256 * i;
-        const bool ok = c < a.cols;
-        if (a.H && ok) {
-            float gv[8], uv[8], h[8];
-            unpack_bf16x8(g[i], gv);
-            unpack_bf16x8(u[i], uv);
+        for (int i = 0; i < 2; ++i) {
+            const int c = c0 + 256 * i;
+            const bool ok = c < a.cols;
+            if (a.H && ok) {
+                float gv[8], uv[8], h[8];
+                unpack_bf16x8(g[i], gv);
+                if (GATED) unpack_bf16x8(u[i], uv);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) h[k] = GATED ? act_value<ACT>(gv[k]) * uv[k] : act_value<ACT>(gv[k]);
-            *reinterpret_cast<uint4 *>(a.H + row * a.ldh + c) = pack_bf16x8(h);
+                for (int k = 0; k < 8; ++k) h[k] = GATED ? act_value<ACT>(gv[k]) * uv[k] : act_value<ACT>(gv[k]);
+                *reinterpret_cast<uint4 *>(a.H + wk.row * a.ldh + c) = pack_bf16x8(h);
+            }
+            if (a.gc) {
+                const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(bf16x8_absmax(g[i])) << 16);
+                if (ok) *reinterpret_cast<uint2 *>(a.gc + wk.row * a.ldc + c) = b8_encode_bf16x8<TYPE>(g[i], b8_inv_scale(byte));
+                gw |= byte << (8 * (2 * i + half));
+            }
+            if (GATED && a.uc) {
+                const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(bf16x8_absmax(u[i])) << 16);
+                if (ok) *reinterpret_cast<uint2 *>(a.uc + wk.row * a.ldc + c) = b8_encode_bf16x8<TYPE>(u[i], b8_inv_scale(byte));
+                uw |= byte << (8 * (2 * i + half));
+            }
         }
         if (a.gc) {
-            const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(bf16x8_absmax(g[i])) << 16);
-            if (ok) *reinterpret_cast<uint2 *>(a.gc + row * a.ldc + c) = b8_encode_bf16x8<TYPE>(g[i], b8_inv_scale(byte));
-            gw |= byte << (8 * (2 * i + half));
+            gw |= __shfl_xor_sync(0xffffffffu, gw, 16);
+            if (lane == 0) a.gs[wi + w * a.rp] = gw;
         }
         if (GATED && a.uc) {
-            const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(bf16x8_absmax(u[i])) << 16);
-            if (ok) *reinterpret_cast<uint2 *>(a.uc + row * a.ldc + c) = b8_encode_bf16x8<TYPE>(u[i], b8_inv_scale(byte));
-            uw |= byte << (8 * (2 * i + half));
+            uw |= __shfl_xor_sync(0xffffffffu, uw, 16);
+            if (lane == 0) a.us[wi + w * a.rp] = uw;
         }
-    }
-    if (a.gc) {
-        gw |= __shfl_xor_sync(0xffffffffu, gw, 16);
-        if (lane == 0) a.gs[wi] = gw;
-    }
-    if (GATED && a.uc) {
-        uw |= __shfl_xor_sync(0xffffffffu, uw, 16);
-        if (lane == 0) a.us[wi] = uw;
     }
 }
 
@@ -146,18 +151,8 @@ struct GluBwdArgs {
     int64_t ldh;
     uint16_t *dG, *dU;
     int64_t ldg, ldu;
-    int32_t rows, cols, words;
+    int32_t rows, cols, words, per_warp;
 };
-
-template <int TYPE>
-__device__ __forceinline__ void b8_load8(const uint2 &q, float s, float (&v)[8])
-{
-    float lo[4], hi[4];
-    b8_decode4<TYPE>(q.x, lo);
-    b8_decode4<TYPE>(q.y, hi);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = __fmul_rn(lo[k], s), v[4 + k] = __fmul_rn(hi[k], s);
-}
 
 template <int TYPE, int ACT, bool GATED>
 __global__ void __launch_bounds__(256) glu_backward_kernel(GluBwdArgs a)
@@ -165,34 +160,42 @@ __global__ void __launch_bounds__(256) glu_backward_kernel(GluBwdArgs a)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, half = lane >> 4;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t row = unit / a.words;
-    const int w = static_cast<int>(unit - row * a.words);
-    if (row >= a.rows) return;
-    const int64_t wi = b8_word_index(w, a.rp, row);
-    const uint32_t gw = __ldg(a.gs + wi), uw = GATED ? __ldg(a.us + wi) : 0u;
-    const int64_t c0 = static_cast<int64_t>(w) * 512 + 128 * half + 8 * (lane & 15);
+    const B8Walk wk = b8_walk(a.words, a.per_warp);
+    if (wk.row >= a.rows) return;
+    const int64_t wi = b8_word_index(0, a.rp, wk.row);
+    const int l0 = 128 * half + 8 * (lane & 15);
+    for (int w = wk.w0; w < wk.w1; ++w) {
+        const int c0 = 512 * w + l0;
+        const uint32_t gw = __ldg(a.gs + wi + w * a.rp), uw = GATED ? __ldg(a.us + wi + w * a.rp) : 0u;
+        uint2 gq[2], uq[2];
+        uint4 hq[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t c = c0 + 256 * i;
-        if (c >= a.cols) continue;
-        const uint2 gq = __ldg(reinterpret_cast<const uint2 *>(a.gc + row * a.ldc + c));
-        const uint2 uq = GATED ? __ldg(reinterpret_cast<const uint2 *>(a.uc + row * a.ldc + c)) : make_uint2(0u, 0u);
-        const uint4 hq = __ldg(reinterpret_cast<const uint4 *>(a.dH + row * a.ldh + c));
-        const int sh = 8 * (2 * i + half);
-        float g[8], u[8], dh[8], dg[8], du[8];
-        b8_load8<TYPE>(gq, b8_scale((gw >> sh) & 0xffu), g);
-        if (GATED) b8_load8<TYPE>(uq, b8_scale((uw >> sh) & 0xffu), u);
-        unpack_bf16x8(hq, dh);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            float v, d;
-            act_value_grad<ACT>(g[k], v, d);
-            dg[k] = GATED ? dh[k] * u[k] * d : dh[k] * d;
-            du[k] = dh[k] * v;
+        for (int i = 0; i < 2; ++i) {
+            const int c = c0 + 256 * i;
+            if (c >= a.cols) continue;
+            gq[i] = __ldg(reinterpret_cast<const uint2 *>(a.gc + wk.row * a.ldc + c));
+            if (GATED) uq[i] = __ldg(reinterpret_cast<const uint2 *>(a.uc + wk.row * a.ldc + c));
+            hq[i] = __ldg(reinterpret_cast<const uint4 *>(a.dH + wk.row * a.ldh + c));
         }
-        *reinterpret_cast<uint4 *>(a.dG + row * a.ldg + c) = pack_bf16x8(dg);
-        if (GATED) *reinterpret_cast<uint4 *>(a.dU + row * a.ldu + c) = pack_bf16x8(du);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = c0 + 256 * i;
+            if (c >= a.cols) continue;
+            const int sh = 8 * (2 * i + half);
+            float g[8], u[8], dh[8], dg[8], du[8];
+            b8_load8<TYPE>(gq[i], b8_scale((gw >> sh) & 0xffu), g);
+            if (GATED) b8_load8<TYPE>(uq[i], b8_scale((uw >> sh) & 0xffu), u);
+            unpack_bf16x8(hq[i], dh);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float v, d;
+                act_value_grad<ACT>(g[k], v, d);
+                dg[k] = GATED ? dh[k] * u[k] * d : dh[k] * d;
+                du[k] = dh[k] * v;
+            }
+            *reinterpret_cast<uint4 *>(a.dG + wk.row * a.ldg + c) = pack_bf16x8(dg);
+            if (GATED) *reinterpret_cast<uint4 *>(a.dU + wk.row * a.ldu + c) = pack_bf16x8(du);
+        }
     }
 }
 
@@ -220,8 +223,8 @@ struct NormBwdArgs {
     float eps;
 };
 
-template <int TYPE, int RT, int NC>
-__global__ void __launch_bounds__(RT > 256 ? RT : 256) norm_backward_kernel(NormBwdArgs a)
+template <int TYPE, int RT, int NC, bool AHEAD>
+__global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 2) norm_backward_kernel(NormBwdArgs a)
 {
     constexpr int kRows = RT >= 256 ? 1 : 256 / RT;  // rows of one step
     constexpr int W = RT / 32;
@@ -231,49 +234,71 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256) norm_backward_kernel(Norm
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int sub = threadIdx.x / RT, lt = threadIdx.x % RT;
     const int chunks = a.K / 8;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    const float invk = 1.0f / static_cast<float>(a.K);
+    uint4 gain[NC];  // bf16 1.0 where there are none
+    const uint8_t *sbase[NC];  // scale byte of the chunk's block, without the row's part
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        const int ci = lt + j * RT, blk = ci >> 4;
+        gain[j] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+        if (a.gain && ci < chunks) gain[j] = __ldg(reinterpret_cast<const uint4 *>(a.gain) + ci);
+        sbase[j] = reinterpret_cast<const uint8_t *>(a.xs) + 4 * (blk >> 2) * a.rp + (blk & 3);
+    }
     float acc[NC][8];
 #pragma unroll
     for (int j = 0; j < NC; ++j)
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[j][k] = 0.0f;
+
+    // a row as it is read; AHEAD: the next one's loads are in flight while this
+    // one is worked on (not with 1024 threads, whose 64 registers would spill)
+    uint2 xq[NC];
+    uint4 du[NC], dr[NC];
+    uint32_t sb[NC];
+    auto load = [&](int64_t row) {
+        const int64_t r127 = row & 127, rpart = 4 * (row - r127 + 4 * (r127 & 31) + (r127 >> 5));
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            const int ci = lt + j * RT;
+            xq[j] = make_uint2(0u, 0u);
+            du[j] = dr[j] = z;
+            sb[j] = 127u;
+            if (row < a.T && ci < chunks) {
+                xq[j] = __ldg(reinterpret_cast<const uint2 *>(a.xc + row * a.ldc) + ci);
+                du[j] = __ldg(reinterpret_cast<const uint4 *>(a.dU + row * a.K) + ci);
+                if (a.dR) dr[j] = *(reinterpret_cast<const uint4 *>(a.dR + row * a.K) + ci);  // dR may be dX
+                sb[j] = __ldg(sbase[j] + rpart);
+            }
+        }
+    };
     int parity = 0;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kRows; base < a.T;
-         base += static_cast<int64_t>(gridDim.x) * kRows, parity ^= 1) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+    int64_t base = static_cast<int64_t>(blockIdx.x) * kRows;
+    if (AHEAD) load(base + sub);
+    for (; base < a.T; base += step, parity ^= 1) {
         const int64_t row = base + sub;
         const bool active = row < a.T;
         float x[NC][8];
-        uint4 du[NC], dr[NC];
+        uint4 cdu[NC], cdr[NC];
         float s1 = 0.0f, s2 = 0.0f;
+        if (!AHEAD) load(row);
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-            const int ci = lt + j * RT;
-            du[j] = dr[j] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[j][k] = 0.0f;
-            if (active && ci < chunks) {
-                const uint2 q = __ldg(reinterpret_cast<const uint2 *>(a.xc + row * a.ldc) + ci);
-                du[j] = __ldg(reinterpret_cast<const uint4 *>(a.dU + row * a.K) + ci);
-                if (a.dR) dr[j] = *(reinterpret_cast<const uint4 *>(a.dR + row * a.K) + ci);  // dR may be dX
-                const int blk = ci >> 4;
-                const uint32_t byte =
-                    __ldg(reinterpret_cast<const uint8_t *>(a.xs + b8_word_index(blk >> 2, a.rp, row)) + (blk & 3));
-                b8_load8<TYPE>(q, b8_scale(byte), x[j]);
-            }
+            b8_load8<TYPE>(xq[j], b8_scale(sb[j]), x[j]);
+            cdu[j] = du[j];
+            cdr[j] = dr[j];
         }
+        if (AHEAD && base + step < a.T) load(row + step);
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-            const int ci = lt + j * RT;
-            float v[8], g[8];
-            unpack_bf16x8(du[j], v);
-            if (a.gain && ci < chunks) {
-                unpack_bf16x8(__ldg(reinterpret_cast<const uint4 *>(a.gain) + ci), g);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] *= g[k];
-            }
+            float d[8], g[8];
+            unpack_bf16x8(cdu[j], d);
+            unpack_bf16x8(gain[j], g);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 s1 = fmaf(x[j][k], x[j][k], s1);
-                s2 = fmaf(v[k], x[j][k], s2);
+                s2 = fmaf(d[k] * x[j][k], g[k], s2);
             }
         }
 #pragma unroll
@@ -294,7 +319,6 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256) norm_backward_kernel(Norm
                 s2 += p.y;
             }
         }
-        const float invk = 1.0f / static_cast<float>(a.K);
         const float r = rsqrtf(s1 * invk + a.eps);
         const float c = r * r * r * (s2 * invk);
         if (!active) continue;
@@ -302,25 +326,14 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256) norm_backward_kernel(Norm
         for (int j = 0; j < NC; ++j) {
             const int ci = lt + j * RT;
             if (ci >= chunks) continue;
-            float v[8], g[8], o[8], d[8];
-            unpack_bf16x8(du[j], v);
+            float d[8], g[8], e[8], o[8];
+            unpack_bf16x8(cdu[j], d);
+            unpack_bf16x8(gain[j], g);
+            unpack_bf16x8(cdr[j], e);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                d[k] = v[k];
-                acc[j][k] = fmaf(v[k] * r, x[j][k], acc[j][k]);
-            }
-            if (a.gain) {
-                unpack_bf16x8(__ldg(reinterpret_cast<const uint4 *>(a.gain) + ci), g);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) d[k] *= g[k];
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = r * d[k] - c * x[j][k];
-            if (a.dR) {
-                float e[8];
-                unpack_bf16x8(dr[j], e);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] += e[k];
+                acc[j][k] = fmaf(d[k] * x[j][k], r, acc[j][k]);
+                o[k] = fmaf(d[k], r * g[k], fmaf(-c, x[j][k], e[k]));
             }
             *(reinterpret_cast<uint4 *>(a.dX + row * a.K) + ci) = pack_bf16x8(o);
         }
