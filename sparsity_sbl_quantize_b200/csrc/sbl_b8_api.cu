@@ -38,10 +38,10 @@ static sbl_status b8_device(HostDevice *hd)
         auto allow = [&](auto kernel) {
             if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kB8SmemAll) != cudaSuccess) st2 = SBL_ERR_CUDA;
         };
-        allow(b8_gemm_kernel<128, false, false>);
-        allow(b8_gemm_kernel<128, false, true>);
-        allow(b8_gemm_kernel<256, true, false>);
-        allow(b8_gemm_kernel<256, true, true>);
+        allow(b8_gemm_kernel<128, false>);
+        allow(b8_gemm_kernel<128, true>);
+        allow(b8_gemm_kernel<256, false>);
+        allow(b8_gemm_kernel<256, true>);
         allow(b8_skinny_kernel<kB8E4M3, 16, true>);
         allow(b8_skinny_kernel<kB8E4M3, 32, true>);
         allow(b8_skinny_kernel<kB8E4M3, 64, true>);
@@ -250,43 +250,37 @@ static bool encode_scales(const HostDevice &hd, CUtensorMap *map, const sbl_b8_d
                      CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-template <int BN, bool PAIR, bool LONG>
+template <int BN, bool LONG>
 static sbl_status launch_b8_gemm(const HostDevice &hd, const sbl_b8_desc *ad, const sbl_b8 *A, const sbl_b8_desc *bd, const sbl_b8 *B,
                                  void *D, int64_t ldd, B8GemmArgs args, cudaStream_t stream)
 {
-    using Cfg = B8Cfg<BN, PAIR>;
-    constexpr int tile_m = PAIR ? 2 * kBM : kBM;
+    using Cfg = B8Cfg<BN>;
     CUtensorMap ta, tb, tsa, tsb, ty;
     const bool fp32 = args.out_fp32 != 0;
-    if (!encode_codes(hd, &ta, ad, A, kBM) || !encode_codes(hd, &tb, bd, B, Cfg::kBRows) ||
+    if (!encode_codes(hd, &ta, ad, A, kBM) || !encode_codes(hd, &tb, bd, B, BN) ||
         !encode_scales(hd, &tsa, ad, A, kBM) || !encode_scales(hd, &tsb, bd, B, BN) ||
         !encode_2d(hd, &ty, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, args.N,
-                   args.M, ldd * (fp32 ? 4 : 2), 32, 32, fp32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   args.M, ldd * (fp32 ? 4 : 2), fp32 ? 16 : 32, 32, CU_TENSOR_MAP_SWIZZLE_64B,
                    CU_TENSOR_MAP_L2_PROMOTION_NONE))
         return SBL_ERR_CUDA;
-    args.tiles_m = static_cast<int32_t>((static_cast<int64_t>(args.M) + tile_m - 1) / tile_m);
+    args.tiles_m = static_cast<int32_t>((static_cast<int64_t>(args.M) + kBM - 1) / kBM);
     args.tiles_n = (args.N + BN - 1) / BN;
     const int64_t tiles = static_cast<int64_t>(args.tiles_m) * args.tiles_n;
     if (tiles > 0x3fffffff) return SBL_ERR_SHAPE;
-    args.idesc = b8_idesc(ad->type, bd->type, tile_m, BN);
+    args.idesc = b8_idesc(ad->type, bd->type, kBM, BN);
     args.err = hd.err;
-    const int units = PAIR ? hd.num_sms / 2 : hd.num_sms;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>((PAIR ? 2 : 1) * std::min<int64_t>(tiles, units)));
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, hd.num_sms)));
     cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = Cfg::kSmemBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, b8_gemm_kernel<BN, PAIR, LONG>, ta, tb, tsa, tsb, ty, args) != cudaSuccess) return SBL_ERR_CUDA;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, b8_gemm_kernel<BN, LONG>, ta, tb, tsa, tsb, ty, args) != cudaSuccess) return SBL_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? SBL_OK : SBL_ERR_CUDA;
 }
 
@@ -424,19 +418,21 @@ static sbl_status gemm(const HostDevice &hd, const sbl_b8_desc *ad, const sbl_b8
         if (!fp32 || p.max_blocks <= kB8SegBlocks)  // longer fp32 sums: see LONG
             return skinny(hd, p, bd, B, ad, nullptr, 0, A, D, ldd, fp32, accumulate, w_early, stream);
     }
-    // 256 x 256 tiles on CTA pairs or 128 x 128 ones on single CTAs: the time
-    // of a launch in units of 0.2 us fits 20 + 2.5 rounds blocks for the
-    // first, 15 + 2 rounds blocks for the second (16384 x 2048 x 11008: 290 against
-    // 473 us; 512 x 6912 x 2560: 13.9 against 19.2; 300 x 4864 x 896: 7.9 against 6.1).
-    auto rounds = [](int64_t m, int64_t n, int64_t t, int64_t units) { return ((m + t - 1) / t * ((n + t - 1) / t) + units - 1) / units; };
-    const int64_t pair_cost = 40 + 5 * rounds(args.M, args.N, 256, hd.num_sms / 2) * args.k_blocks;
-    const int64_t one_cost = 30 + 4 * rounds(args.M, args.N, 128, hd.num_sms) * args.k_blocks;
+    // 128 x 256 tiles or 128 x 128 ones, of which a product with few tiles has
+    // twice as many: the time of a launch in units of 10 ns fits
+    // 460 + rounds (42 blocks + 60) and 340 + rounds (34 blocks + 45)
+    // (16384 x 2048 x 11008: 269 against 440 us; 512 x 6912 x 2560: 14.0 against 18.3;
+    // 300 x 4864 x 896: 6.6 against 5.9; 777 x 1536 x 1536: 8.5 against 8.0).
+    auto rounds = [&](int64_t bn) {
+        return ((static_cast<int64_t>(args.M) + kBM - 1) / kBM * ((args.N + bn - 1) / bn) + hd.num_sms - 1) / hd.num_sms;
+    };
+    const bool wide = 460 + rounds(256) * (42ll * args.k_blocks + 60) <= 340 + rounds(128) * (34ll * args.k_blocks + 45);
     const bool lng = fp32 && args.k_blocks > kB8SegBlocks;
-    if (pair_cost <= one_cost)
-        return lng ? launch_b8_gemm<256, true, true>(hd, ad, A, bd, B, D, ldd, args, stream)
-                   : launch_b8_gemm<256, true, false>(hd, ad, A, bd, B, D, ldd, args, stream);
-    return lng ? launch_b8_gemm<128, false, true>(hd, ad, A, bd, B, D, ldd, args, stream)
-               : launch_b8_gemm<128, false, false>(hd, ad, A, bd, B, D, ldd, args, stream);
+    if (wide)
+        return lng ? launch_b8_gemm<256, true>(hd, ad, A, bd, B, D, ldd, args, stream)
+                   : launch_b8_gemm<256, false>(hd, ad, A, bd, B, D, ldd, args, stream);
+    return lng ? launch_b8_gemm<128, true>(hd, ad, A, bd, B, D, ldd, args, stream)
+               : launch_b8_gemm<128, false>(hd, ad, A, bd, B, D, ldd, args, stream);
 }
 
 // The workspace of sbl_b8_linear_backward: dY in both block orders and X

@@ -13,8 +13,15 @@
 // every stage's partial sum would have to leave tensor memory to be scaled in
 // registers: 64 FMAs and TMEM reads per SM and clock beside the MMAs.
 //
-// Tiles and roles are those of the other tcgen05 products: warp 0 TMA loads,
-// warp 1 MMAs, warps 2-9 the epilogue.
+// Tiles are 128 x BN (256, or 128 where that spreads a small product over more
+// SMs); roles as in the other tcgen05 products: warp 0 TMA loads, warp 1 MMAs,
+// warps 2-9 the epilogue.  CTA pairs with 256 x 256 tiles were built too and
+// measured no faster anywhere (16384 x 11008 x 2048: 309 us against 299,
+// 16384 x 2048 x 11008: 296 against 269), so there are none.
+//
+// 16384 x 2048 x 11008 takes 269 us, 2.7 PFLOP/s (twice the measured sustained
+// bf16 rate); the same MMAs without loads or scales take 232: the rest is the
+// tensor core waiting between stages and tiles.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -35,11 +42,17 @@ struct B8GemmArgs {
     uint32_t *err;
 };
 
-// Columns of tensor memory: two accumulators of BN columns, then kB8SfBufs
-// buffers of scale words (4 columns for 128 A rows, 4 per 128 B rows).  Four
-// buffers in turn put 16 stages between two uses of a buffer, more than the
-// ring holds, so a copy never meets MMAs that still read the old scales.
-constexpr int kB8SfBufs = 4;
+// Scales move in groups of kB8SfBlocks K blocks (two words a row): every copy
+// to tensor memory makes the MMAs behind it wait, and a copy of two words costs
+// little more than one (without loads, 16384 x 2048 x 11008 took 245 us with one
+// word a copy, 231 with two, 235 without any copy).  Two groups have room, in
+// shared memory (where a slot is loaded) and in tensor memory next to the two
+// accumulators of BN columns (4 columns for 128 A rows, 4 per 128 B rows, a word).
+constexpr int kB8SfBlocks = 8;
+constexpr int kB8SfBufs = 2;
+// Epilogue staging: one block of 32 rows x 64 bytes per epilogue warp.
+constexpr int kB8EpiBufBytes = 32 * 64;
+constexpr int kB8EpiBytes = kEpiWarps * kB8EpiBufBytes;
 
 // A kernel that takes c of the 512 columns of tensor memory takes at least
 // c / 512 of the SM's shared memory too (all of it here).  Then CTAs that fit
@@ -48,24 +61,25 @@ constexpr int kB8SfBufs = 4;
 // while both wait for cluster mates elsewhere, could close a circle.
 constexpr int kB8SmemAll = 227 * 1024;
 
-template <int BN, bool PAIR>
+template <int BN>
 struct B8Cfg {
     static_assert(BN == 128 || BN == 256, "tile width");
-    static constexpr int kBRows = PAIR ? BN / 2 : BN;
-    static constexpr int kBBytes = kBRows * kBKBytes;
+    static constexpr int kBBytes = BN * kBKBytes;
     static constexpr int kSfaBytes = 512;
     static constexpr int kSfbBytes = BN * 4;
-    static constexpr int kSfBytes = kSfaBytes + kSfbBytes;
+    static constexpr int kSfWordBytes = kSfaBytes + kSfbBytes;  // one word of every row
+    static constexpr int kSfBytes = kB8SfBlocks / 4 * kSfWordBytes;
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = (180 * 1024) / (kStageBytes + kSfBytes);
-    static constexpr int kSfCols = 4 + BN / 32;
+    // six, or four of the 48 KiB ones; five instead of six measured the same
+    static constexpr int kStages = (kB8SmemAll - 1024 - kB8EpiBytes - kB8SfBufs * kSfBytes - 256) / kStageBytes;
+    static constexpr int kSfWordCols = 4 + BN / 32;
+    static constexpr int kSfCols = kB8SfBlocks / 4 * kSfWordCols;
     static constexpr int kSfCol0 = kTmemCols - kB8SfBufs * kSfCols;
     // second accumulator: next to the first, or overlapping its last columns
     // where two do not fit beside the scales (see the epilogue)
     static constexpr int kAcc1 = 2 * BN <= kSfCol0 ? BN : (kSfCol0 - BN) / 32 * 32;
     static constexpr int kOverlap = BN - kAcc1;  // columns shared by the accumulators
     static_assert(kOverlap <= 64, "the first drained columns must free the overlap");
-    static_assert(1024 + kStages * (kStageBytes + kSfBytes) + kEpiBytes + 256 <= kB8SmemAll, "shared memory");
     static constexpr int kSmemBytes = kB8SmemAll;
 };
 
@@ -84,30 +98,20 @@ __device__ __forceinline__ uint32_t b8_idesc_with_block(uint32_t idesc, int kb)
     return idesc | (id << 4) | (id << 29);
 }
 
-template <bool PAIR>
 __device__ __forceinline__ void mma_b8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa,
                                        uint32_t sfb, uint32_t accumulate)
 {
-    if constexpr (PAIR)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
 }
 
 // 512 bytes of scale words (128 rows x 4 blocks) to four columns of tensor
 // memory, the same in each 32-lane quarter: 32 rows of 16 bytes, 8-row groups
 // 128 bytes apart, no swizzle.
-template <bool PAIR>
 __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t saddr)
 {
     uint64_t d = 0;
@@ -115,11 +119,29 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t saddr)
     d |= static_cast<uint64_t>(1u) << 16;
     d |= static_cast<uint64_t>(128u >> 4) << 32;
     d |= static_cast<uint64_t>(1u) << 46;
-    if constexpr (PAIR)
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
-    else
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
+
+// Which stage last used each of the kB8SfBufs slots of a group ring: slots are
+// taken in turn, so the oldest use is the next slot's.
+struct SfUse {
+    static_assert(kB8SfBufs == 2, "two slots");
+    uint32_t groups = 0;             // groups so far
+    uint32_t last[2] = {0u, 0u};     // 1 + stage of the slot's last use (0: none), oldest first
+    __device__ __forceinline__ uint32_t slot() const { return groups & 1u; }
+    __device__ __forceinline__ uint32_t oldest() const { return last[0] - 1u; }
+    // the next slot was used fewer than `ring` stages before stage `now`
+    __device__ __forceinline__ bool recent(uint32_t now, int ring) const
+    {
+        return last[0] != 0u && now - oldest() < static_cast<uint32_t>(ring);
+    }
+    __device__ __forceinline__ void use(uint32_t stage)
+    {
+        last[0] = last[1];
+        last[1] = stage + 1u;
+        ++groups;
+    }
+};
 
 // D += block (fp32, element-wise in L2; each element of D gets one addition
 // per launch, so the result does not depend on the order).
@@ -142,16 +164,15 @@ constexpr int kB8SegBlocks = 32;
 // summed in tensor memory and then added in registers with rounding.
 //
 // tmSA, tmSB: the scale words as [ceil(blocks / 4), padded rows] of 32 bits,
-// boxes of 128 (A) and BN (B) words: both CTAs of a pair need every B scale.
-template <int BN, bool PAIR, bool LONG>
+// boxes of 128 (A) and BN (B) words.
+template <int BN, bool LONG>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     b8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                    const __grid_constant__ CUtensorMap tmY, B8GemmArgs args)
 {
-    using Cfg = B8Cfg<BN, PAIR>;
+    using Cfg = B8Cfg<BN>;
     constexpr int kStages = Cfg::kStages;
-    constexpr int kTileM = PAIR ? 2 * kBM : kBM;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -159,22 +180,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t a_base = base;
     const uint32_t b_base = a_base + kStages * kABytes;
     const uint32_t epi_base = b_base + kStages * Cfg::kBBytes;
-    const uint32_t sf_base = epi_base + kEpiBytes;
-    const uint32_t bar_base = sf_base + kStages * Cfg::kSfBytes;
+    const uint32_t sf_base = epi_base + kB8EpiBytes;
+    const uint32_t bar_base = sf_base + kB8SfBufs * Cfg::kSfBytes;
     auto full_bar = [&](int s) { return bar_base + 8u * s; };
     auto empty_bar = [&](int s) { return bar_base + 8u * (kStages + s); };
     auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * kStages + a); };
     auto tempty_bar = [&](int a) { return bar_base + 8u * (2 * kStages + 2 + a); };
     const uint32_t drain_bar = bar_base + 8u * (2 * kStages + 4);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base_ptr + (bar_base - base) + 224);
-    static_assert(8 * (2 * kStages + 5) <= 224, "barriers");
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base_ptr + (drain_bar + 8u - base));
+    static_assert(8 * (2 * kStages + 6) <= 256, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int num_tiles = args.tiles_m * args.tiles_n;
-    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
-    const bool leader = rank == 0;
-    const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
-    const int units = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
+    const int unit = static_cast<int>(blockIdx.x), units = static_cast<int>(gridDim.x);
     const int segments = LONG ? (args.k_blocks + kB8SegBlocks - 1) / kB8SegBlocks : 1;
 
     if (threadIdx.x == 0) {
@@ -184,7 +202,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull_bar(a), 1);
-            mbar_init(tempty_bar(a), (PAIR ? 2 : 1) * kEpiWarps);  // one arrival per epilogue warp
+            mbar_init(tempty_bar(a), kEpiWarps);  // one arrival per epilogue warp
         }
         mbar_init(drain_bar, 1);
         fence_barrier_init();
@@ -195,18 +213,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tma_prefetch_map(&tmY);
     }
     if (warp == 1) {
-        if constexpr (PAIR) {
-            tmem_alloc_pair(smem_addr(tmem_slot), kTmemCols);
-            tmem_relinquish_pair();
-        } else {
-            tmem_alloc(smem_addr(tmem_slot), kTmemCols);
-            tmem_relinquish();
-        }
+        tmem_alloc(smem_addr(tmem_slot), kTmemCols);
+        tmem_relinquish();
         tc_fence_before();
     }
     __syncthreads();
     tc_fence_after();
-    if constexpr (PAIR) cluster_sync_all();
     const uint32_t tmem_base = *tmem_slot;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -219,127 +231,146 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         uint32_t issued_mask = 0;
         uint32_t issued_phase[kStages];
         for (int s = 0; s < kStages; ++s) issued_phase[s] = 0;
+        // Scales come with the first stage of their group.  A slot may be
+        // filled again when the copy that read it, issued with the first stage
+        // of group - kB8SfBufs, has finished: known from the ring if that
+        // stage lies kStages back, else waited for.
+        SfUse used;
+        uint32_t count = 0;  // stages so far
         for (int tile = unit; ok && tile < num_tiles; tile += units) {
             int tm, tn;
             tile_coords(tile, args.tiles_m, args.tiles_n, tm, tn);
-            const int arow = tm * kTileM + static_cast<int>(rank) * kBM;
-            const int brow = tn * BN + static_cast<int>(rank) * Cfg::kBRows;
+            const int arow = tm * kBM;
+            const int brow = tn * BN;
             for (int kb = 0; kb < args.k_blocks; ++kb) {
                 const bool ready = mbar_wait(empty_bar(stage), phase ^ 1u, args.err, kErrB8Gemm);
                 if (!__all_sync(0xffffffffu, ready)) {
                     ok = false;
                     break;
                 }
-                if (lane == 0) {
-                    const bool sf = (kb & 3) == 0;  // this stage brings the scales of four
-                    const uint32_t bytes = Cfg::kStageBytes + (sf ? Cfg::kSfBytes : 0);
-                    const uint32_t sa = sf_base + stage * Cfg::kSfBytes, sb = sa + Cfg::kSfaBytes;
-                    if constexpr (PAIR) {
-                        const uint32_t fb = map_shared_rank(full_bar(stage), 0);
-                        if (leader) mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
-                        tma_load_2d_pair(a_base + stage * kABytes, &tmA, kb * 128, arow, fb);
-                        tma_load_2d_pair(b_base + stage * Cfg::kBBytes, &tmB, kb * 128, brow, fb);
-                        if (sf) {
-                            tma_load_2d_pair(sa, &tmSA, arow, kb >> 2, fb);
-                            tma_load_2d_pair(sb, &tmSB, tn * BN, kb >> 2, fb);
-                        }
-                    } else {
-                        mbar_arrive_expect_tx(full_bar(stage), bytes);
-                        tma_load_2d(a_base + stage * kABytes, &tmA, kb * 128, arow, full_bar(stage));
-                        tma_load_2d(b_base + stage * Cfg::kBBytes, &tmB, kb * 128, brow, full_bar(stage));
-                        if (sf) {
-                            tma_load_2d(sa, &tmSA, arow, kb >> 2, full_bar(stage));
-                            tma_load_2d(sb, &tmSB, tn * BN, kb >> 2, full_bar(stage));
+                const bool sf = kb % kB8SfBlocks == 0;
+                if (sf) {
+                    if (used.recent(count, kStages)) {
+                        const uint32_t st = used.oldest();
+                        const bool copied = mbar_wait(empty_bar(st % kStages), (st / kStages) & 1u, args.err, kErrB8Gemm);
+                        if (!__all_sync(0xffffffffu, copied)) {
+                            ok = false;
+                            break;
                         }
                     }
                 }
+                if (lane == 0) {
+                    const int words = sf ? min(kB8SfBlocks / 4, (args.k_blocks - kb + 3) >> 2) : 0;
+                    const uint32_t bytes = Cfg::kStageBytes + words * Cfg::kSfWordBytes;
+                    const uint32_t s = sf_base + used.slot() * Cfg::kSfBytes;
+                    const uint32_t fb = full_bar(stage);
+                    mbar_arrive_expect_tx(fb, bytes);
+                    tma_load_2d(a_base + stage * kABytes, &tmA, kb * 128, arow, fb);
+                    tma_load_2d(b_base + stage * Cfg::kBBytes, &tmB, kb * 128, brow, fb);
+                    for (int w = 0; w < words; ++w) {
+                        tma_load_2d(s + w * Cfg::kSfWordBytes, &tmSA, arow, (kb >> 2) + w, fb);
+                        tma_load_2d(s + w * Cfg::kSfWordBytes + Cfg::kSfaBytes, &tmSB, tn * BN, (kb >> 2) + w, fb);
+                    }
+                }
+                if (sf) used.use(count);
+                ++count;
                 __syncwarp();
                 issued_mask |= 1u << stage;
                 issued_phase[stage] = phase;
                 if (++stage == kStages) stage = 0, phase ^= 1u;
             }
         }
-        if (!ok && leader) {
+        if (!ok) {
+            // loads still in flight land before the CTA can exit
             for (int s = 0; s < kStages; ++s)
                 if (issued_mask & (1u << s)) mbar_wait(full_bar(s), issued_phase[s], args.err, kErrB8Gemm);
         }
-    } else if (warp == 1 && leader) {
+    } else if (warp == 1) {
         // -------------------------------------------------------- MMA issuer
+        // Whole-warp control flow with one elected lane issuing: the
+        // instructions want uniform registers, and what the compiler makes of a
+        // lane-0 branch cost 5% (16384 x 2048 x 11008: 288 us against 269), the
+        // same loop in one thread 14%.
+        const bool elected = elect_one();
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
         int local = 0;
-        uint32_t sf_group = 0;  // groups of four stages so far
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, args.err, kErrB8Gemm)) != 0;
+        };
+        // A buffer of scales may be written again when the MMAs that read it
+        // have finished (the last stage of group - kB8SfBufs).
+        SfUse read;
+        uint32_t count = 0, sfa = 0;
         for (int tile = unit; ok && tile < num_tiles; tile += units) {
             for (int seg = 0; ok && seg < segments; ++seg, ++local) {
                 const int kb0 = LONG ? seg * kB8SegBlocks : 0;
                 const int kb1 = LONG ? min(kb0 + kB8SegBlocks, args.k_blocks) : args.k_blocks;
                 const int acc = local & 1;
-                // The accumulator's columns are free: with two disjoint ones when
-                // tile local - 2 is drained; with overlapping ones when the first
-                // columns of tile local - 1 are (all of local - 2 is by then).
-                bool free_acc = true;
+                // The accumulator's columns are free: with two disjoint ones
+                // when tile local - 2 is drained; with overlapping ones when the
+                // first columns of tile local - 1 are (all of local - 2 is by
+                // then).
                 if constexpr (Cfg::kOverlap > 0) {
-                    if (local >= 1)
-                        free_acc = mbar_wait(tempty_bar(acc ^ 1), ((local - 1) >> 1) & 1, args.err, kErrB8Gemm);
+                    if (local >= 1) ok = wait(tempty_bar(acc ^ 1), ((local - 1) >> 1) & 1);
                 } else {
-                    free_acc = mbar_wait(tempty_bar(acc), ((local >> 1) & 1) ^ 1, args.err, kErrB8Gemm);
+                    ok = wait(tempty_bar(acc), ((local >> 1) & 1) ^ 1);
                 }
-                if (!__all_sync(0xffffffffu, free_acc)) {
-                    ok = false;
-                    break;
-                }
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * Cfg::kAcc1);
-                uint32_t sfa = 0;
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    const bool ready = mbar_wait(full_bar(stage), phase, args.err, kErrB8Gemm);
-                    if (!__all_sync(0xffffffffu, ready)) {
-                        ok = false;
-                        break;
+                    ok = wait(full_bar(stage), phase);
+                    if (!ok) break;
+                    const bool sf = kb % kB8SfBlocks == 0;
+                    if (sf) {
+                        if (read.recent(count, kStages)) {
+                            const uint32_t st = read.oldest();
+                            ok = wait(empty_bar(st % kStages), (st / kStages) & 1u);
+                            if (!ok) break;
+                        }
+                        sfa = tmem_base + Cfg::kSfCol0 + read.slot() * Cfg::kSfCols;
                     }
                     tc_fence_after();
-                    if ((kb & 3) == 0) {
-                        sfa = tmem_base + Cfg::kSfCol0 + (sf_group % kB8SfBufs) * Cfg::kSfCols;
-                        ++sf_group;
-                    }
-                    if (lane == 0) {
-                        if ((kb & 3) == 0) {
-                            const uint32_t s = sf_base + stage * Cfg::kSfBytes;
-                            tmem_cp_scales<PAIR>(sfa, s);
+                    const uint32_t sft = sfa + ((kb % kB8SfBlocks) >> 2) * Cfg::kSfWordCols;
+                    const uint32_t idesc = b8_idesc_with_block(args.idesc, kb);
+                    const uint64_t adesc = smem_desc_k128(a_base + stage * kABytes);
+                    const uint64_t bdesc = smem_desc_k128(b_base + stage * Cfg::kBBytes);
+                    if (elected) {
+                        if (sf) {
+                            const uint32_t s = sf_base + read.slot() * Cfg::kSfBytes;
 #pragma unroll
-                            for (int i = 0; i < BN / 128; ++i)
-                                tmem_cp_scales<PAIR>(sfa + 4 + 4 * i, s + Cfg::kSfaBytes + 512 * i);
+                            for (int w = 0; w < kB8SfBlocks / 4; ++w) {
+                                if (kb + 4 * w >= args.k_blocks) break;
+                                const uint32_t t = sfa + w * Cfg::kSfWordCols, sw = s + w * Cfg::kSfWordBytes;
+                                tmem_cp_scales(t, sw);
+#pragma unroll
+                                for (int i = 0; i < BN / 128; ++i) tmem_cp_scales(t + 4 + 4 * i, sw + Cfg::kSfaBytes + 512 * i);
+                            }
                         }
-                        const uint32_t idesc = b8_idesc_with_block(args.idesc, kb);
-                        const uint64_t adesc = smem_desc_k128(a_base + stage * kABytes);
-                        const uint64_t bdesc = smem_desc_k128(b_base + stage * Cfg::kBBytes);
 #pragma unroll
                         for (int kk = 0; kk < kBKBytes / 32; ++kk)
-                            mma_b8<PAIR>(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, sfa, sfa + 4, (kb > kb0 || kk > 0) ? 1u : 0u);
-                        if constexpr (PAIR)
-                            tc_commit_pair(empty_bar(stage), 0x3);
-                        else
-                            tc_commit(empty_bar(stage));
+                            mma_b8(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, sft, sft + 4, (kb > kb0 || kk > 0) ? 1u : 0u);
+                        // frees the stage (and the scales' slot) once these finish
+                        tc_commit(empty_bar(stage));
                     }
                     __syncwarp();
+                    // the group's last stage (of this tile) closes its buffer
+                    if (kb % kB8SfBlocks == kB8SfBlocks - 1 || kb == args.k_blocks - 1) read.use(count);
+                    ++count;
                     if (++stage == kStages) stage = 0, phase ^= 1u;
                 }
                 if (!ok) break;
-                if (lane == 0) {
-                    if constexpr (PAIR)
-                        tc_commit_pair(tfull_bar(acc), 0x3);
-                    else
-                        tc_commit(tfull_bar(acc));
+                if (elected) {
+                    tc_commit(tfull_bar(acc));
                 }
                 __syncwarp();
             }
         }
-        if (lane == 0) {
-            if constexpr (PAIR)
-                tc_commit_pair(drain_bar, 0x1);
-            else
-                tc_commit(drain_bar);
+        // every MMA issued has completed before tensor memory is released
+        if (elected) {
+            tc_commit(drain_bar);
         }
         __syncwarp();
         mbar_wait(drain_bar, 0, args.err, kErrB8Gemm);
@@ -352,66 +383,60 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         // the first 64 of the second, and the next tile's MMAs may start.
         const int quarter = warp & 3;
         const int half = (warp - 2) >> 2;
-        const uint32_t buf = epi_base + static_cast<uint32_t>(warp - 2) * kEpiBufBytes;
+        const uint32_t buf = epi_base + static_cast<uint32_t>(warp - 2) * kB8EpiBufBytes;
         constexpr int kChunks = BN / 64;
-        uint32_t nstore = 0;
         int local = 0;
         auto release = [&](int acc) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if constexpr (PAIR)
-                    mbar_arrive_cluster(map_shared_rank(tempty_bar(acc), 0));
-                else
-                    mbar_arrive(tempty_bar(acc));
+                mbar_arrive(tempty_bar(acc));
             }
         };
-        // 32 x 32 fp32 values of this warp to D (staged, swizzled, one TMA store)
-        auto store = [&](const uint32_t(&v)[32], int col, int row0) {
-            if (col >= args.N || row0 >= args.M) return;  // warp-uniform: block outside D
-            if (!args.out_fp32) {
-                // two 2 KiB staging halves in turn: rows of 64 bytes, chunk c
-                // at c ^ ((lane / 2) % 4) (64-byte swizzle)
-                const uint32_t sbuf = buf + static_cast<uint32_t>((nstore & 1) * (kEpiBufBytes / 2));
-                if (lane == 0) bulk_wait_group_read<1>();
-                __syncwarp();
+        // one staged block: 32 rows of 64 bytes, 16-byte chunk c at
+        // c ^ ((lane / 2) % 4) (64-byte swizzle), one TMA store
+        auto store_block = [&](const uint32_t(&w)[16], int col, int row0) {
+            if (lane == 0) bulk_wait_group_read<0>();  // the block before has left the buffer
+            __syncwarp();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) w[q] = pack_bf16(__uint_as_float(v[8 * c + 2 * q]), __uint_as_float(v[8 * c + 2 * q + 1]));
-                    const uint32_t addr = sbuf + static_cast<uint32_t>(lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16));
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                                 : "memory");
-                }
-            } else {
-                if (lane == 0) bulk_wait_group_read<0>();
-                __syncwarp();
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint32_t addr = buf + static_cast<uint32_t>(lane * 128 + ((c ^ (lane & 7)) * 16));
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[4 * c]), "r"(v[4 * c + 1]),
-                                 "r"(v[4 * c + 2]), "r"(v[4 * c + 3])
-                                 : "memory");
-                }
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t addr = buf + static_cast<uint32_t>(lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16));
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[4 * c]), "r"(w[4 * c + 1]),
+                             "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                             : "memory");
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                if (!args.out_fp32)
-                    tma_store_2d(&tmY, buf + static_cast<uint32_t>((nstore & 1) * (kEpiBufBytes / 2)), col, row0);
-                else if (args.accumulate)
+                if (args.accumulate)
                     tma_reduce_add_2d(&tmY, buf, col, row0);
                 else
                     tma_store_2d(&tmY, buf, col, row0);
                 bulk_commit_group();
             }
-            ++nstore;
+        };
+        // 32 rows x 32 columns of this warp: one block in bf16, two in fp32
+        auto store = [&](const uint32_t(&v)[32], int col, int row0) {
+            if (col >= args.N || row0 >= args.M) return;  // warp-uniform: block outside D
+            uint32_t w[16];
+            if (!args.out_fp32) {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) w[q] = pack_bf16(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
+                store_block(w, col, row0);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (col + 16 * h >= args.N) break;
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) w[q] = v[16 * h + q];
+                    store_block(w, col + 16 * h, row0);
+                }
+            }
         };
         for (int tile = unit; tile < num_tiles; tile += units) {
             int tm, tn;
             tile_coords(tile, args.tiles_m, args.tiles_n, tm, tn);
-            const int row0 = tm * kTileM + static_cast<int>(rank) * kBM + quarter * 32;
+            const int row0 = tm * kBM + quarter * 32;
             const int col0 = tn * BN + 32 * half;
             if constexpr (LONG) {
                 float sum[kChunks][32];
@@ -478,14 +503,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
 
     __syncthreads();
-    if constexpr (PAIR) cluster_sync_all();
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        if constexpr (PAIR)
-            tmem_dealloc_pair(tmem_base, kTmemCols);
-        else
-            tmem_dealloc(tmem_base, kTmemCols);
+        tmem_dealloc(tmem_base, kTmemCols);
     }
 }
 

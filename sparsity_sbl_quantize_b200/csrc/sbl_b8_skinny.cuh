@@ -172,24 +172,25 @@ __global__ void __launch_bounds__(kSkThreads)
         }
     } else if (warp == 1) {
         // -------------------------------------------------------- MMA issuer
+        const bool elected = elect_one();
         const uint32_t sf_tmem = tmem_base + NT;
-        bool ok = mbar_wait(sf_bar, 0, args.err, kErrB8Gemm);
-        if (FUSED && ok) ok = mbar_wait(x_bar, 0, args.err, kErrB8Gemm);
+        bool ok = mbar_wait_spin(sf_bar, 0, args.err, kErrB8Gemm);
+        if (FUSED && ok) ok = mbar_wait_spin(x_bar, 0, args.err, kErrB8Gemm);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
-        if (ok && lane == 0)
+        if (ok && elected)
             for (int g = 0; g < groups; ++g) {
-                tmem_cp_scales<false>(sf_tmem + 8 * g, sfw_base + 512 * g);
-                tmem_cp_scales<false>(sf_tmem + 8 * g + 4, sfx_base + 512 * g);
+                tmem_cp_scales(sf_tmem + 8 * g, sfw_base + 512 * g);
+                tmem_cp_scales(sf_tmem + 8 * g + 4, sfx_base + 512 * g);
             }
         __syncwarp();
         int stage = 0;
         uint32_t phase = 0;
         for (int b = b0; ok && b < b1; ++b) {
-            ok = __all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, args.err, kErrB8Gemm));
+            ok = __all_sync(0xffffffffu, mbar_wait_spin(full_bar(stage), phase, args.err, kErrB8Gemm));
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
+            if (elected) {
                 const uint32_t s = base + stage * kStageBytes;
                 const uint32_t sf = sf_tmem + 8 * ((b >> 2) - g0);
                 const uint32_t idesc = b8_idesc_with_block(args.idesc, b);
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kSkThreads)
                 const uint64_t xdesc = smem_desc_k128(FUSED ? x_base + (b - b0) * NT * kBKBytes : s + kABytes);
 #pragma unroll
                 for (int kk = 0; kk < kBKBytes / 32; ++kk)
-                    mma_b8<false>(tmem_base, wdesc + 2 * kk, xdesc + 2 * kk, idesc, sf, sf + 4, (b > b0 || kk > 0) ? 1u : 0u);
+                    mma_b8(tmem_base, wdesc + 2 * kk, xdesc + 2 * kk, idesc, sf, sf + 4, (b > b0 || kk > 0) ? 1u : 0u);
                 tc_commit(empty_bar(stage));
             }
             __syncwarp();
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(kSkThreads)
         }
         // every MMA issued has completed: the epilogue's signal, and before
         // tensor memory is released
-        if (lane == 0) tc_commit(done_bar);
+        if (elected) tc_commit(done_bar);
         __syncwarp();
     } else if constexpr (FUSED) {
         // ------------------------------------ quantise X's part (warps 2-7)
