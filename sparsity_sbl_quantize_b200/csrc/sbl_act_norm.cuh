@@ -69,7 +69,10 @@ struct NormCkpt {
     int32_t words;  // scale words per row
 };
 
-template <int RT, int CK = kNoCkpt>
+//
+// NC: 16-byte chunks a thread holds.  With a checkpoint 4 (twice the threads a
+// row): the scaled row then fits in registers and is computed once.
+template <int RT, int CK = kNoCkpt, int NC = kActMaxChunks>
 __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 3)
     act_norm_quant_kernel(const uint16_t *__restrict__ X, int32_t T, int32_t K, const uint16_t *__restrict__ g,
                           double eps, int8_t *__restrict__ Xq, float *__restrict__ d, NormCkpt ck)
@@ -89,9 +92,9 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 3)
     const bool active = row < T;
     const int chunks = K / 8;
 
-    uint4 v[kActMaxChunks];
+    uint4 v[NC];
 #pragma unroll
-    for (int c = 0; c < kActMaxChunks; ++c) {
+    for (int c = 0; c < NC; ++c) {
         const int ci = lt + c * RT;
         v[c] = make_uint4(0u, 0u, 0u, 0u);
         if (active && ci < chunks) v[c] = __ldg(reinterpret_cast<const uint4 *>(X + row * K) + ci);
@@ -99,7 +102,7 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 3)
     if constexpr (CK != kNoCkpt) {
         uint8_t *sb = reinterpret_cast<uint8_t *>(ck.scales);
 #pragma unroll
-        for (int c = 0; c < kActMaxChunks; ++c) {
+        for (int c = 0; c < NC; ++c) {
             const int ci = lt + c * RT;
             const uint32_t byte = b8_scale_byte<CK>(half_warp_max(bf16x8_absmax(v[c])) << 16);
             if (active && ci < chunks) {
@@ -115,6 +118,8 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 3)
     double cs[kActMaxChunks];
 #pragma unroll
     for (int c = 0; c < kActMaxChunks; ++c) {
+        cs[c] = 0.0;  // a slot past the held chunks: +0.0 leaves the tree's sums exact
+        if (c >= NC) continue;
         const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
         double sq[8];
 #pragma unroll
@@ -173,15 +178,21 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 3)
     __syncthreads();
     const float r = rsh[sub];
 
-    // u = fl32(fl32(x * r) * g), computed from the held x in both passes:
-    // max|u| over the row, then the quantised stores
+    // u = fl32(fl32(x * r) * g), computed from the held x in both passes (held
+    // itself where a thread has few chunks): max|u| over the row, then the
+    // quantised stores
+    constexpr bool kKeep = NC <= 4;
+    float held[kKeep ? NC : 1][8];
     float amax = 0.0f;
 #pragma unroll
-    for (int c = 0; c < kActMaxChunks; ++c) {
+    for (int c = 0; c < NC; ++c) {
         float u[8];
         norm_chunk(v[c], g, lt + c * RT, chunks, r, u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(u[i]));
+        for (int i = 0; i < 8; ++i) {
+            amax = fmaxf(amax, fabsf(u[i]));
+            if (kKeep) held[kKeep ? c : 0][i] = u[i];
+        }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
@@ -195,13 +206,18 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 3)
     // with a checkpoint the factor is 127 * (1 / a), two roundings (sbl.h)
     const float rq = zero ? 0.0f : CK == kNoCkpt ? __fdiv_rn(127.0f, amax) : __fmul_rn(127.0f, __frcp_rn(amax));
 #pragma unroll
-    for (int c = 0; c < kActMaxChunks; ++c) {
+    for (int c = 0; c < NC; ++c) {
         const int ci = lt + c * RT;
         if (ci >= chunks) continue;
         uint2 out = make_uint2(0u, 0u);
         if (!zero) {
             float u[8];
-            norm_chunk(v[c], g, ci, chunks, r, u);
+            if constexpr (kKeep) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = held[c][i];
+            } else {
+                norm_chunk(v[c], g, ci, chunks, r, u);
+            }
             out.x = quant4(u[0], u[1], u[2], u[3], rq);
             out.y = quant4(u[4], u[5], u[6], u[7], rq);
         }

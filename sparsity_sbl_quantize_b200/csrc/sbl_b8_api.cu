@@ -266,7 +266,8 @@ static sbl_status launch_b8_gemm(const HostDevice &hd, const sbl_b8_desc *ad, co
     args.tiles_m = static_cast<int32_t>((static_cast<int64_t>(args.M) + kBM - 1) / kBM);
     args.tiles_n = (args.N + BN - 1) / BN;
     const int64_t tiles = static_cast<int64_t>(args.tiles_m) * args.tiles_n;
-    if (tiles > 0x3fffffff) return SBL_ERR_SHAPE;
+    // 32-bit tile numbers and, per CTA, stage counts
+    if (tiles > 0x3fffffff || (tiles / hd.num_sms + 1) * args.k_blocks > 0x7fffffff) return SBL_ERR_SHAPE;
     args.idesc = b8_idesc(ad->type, bd->type, kBM, BN);
     args.err = hd.err;
     cudaLaunchConfig_t cfg;
@@ -312,8 +313,6 @@ static SkinnyPlan skinny_plan(int num_sms, int32_t O, int32_t K, int32_t T, bool
     p.tmem_cols = 32;
     while (p.tmem_cols < p.nt + 8 * p.max_groups) p.tmem_cols *= 2;
     p.smem = fixed + p.stages * skinny_stage_bytes(p.nt, fused);
-    // shared memory in proportion to tensor memory (see kB8SmemAll)
-    p.smem = std::max<int64_t>(p.smem, static_cast<int64_t>(p.tmem_cols) * kB8SmemAll / kTmemCols);
     return p;
 }
 
@@ -469,28 +468,32 @@ template <int TYPE>
 static sbl_status norm_checkpoint(const uint16_t *X, int32_t T, int32_t K, const uint16_t *g, double eps, int8_t *Xq, float *d,
                                   NormCkpt ck, cudaStream_t stream)
 {
+    // four chunks a thread up to 256 threads a row, eight beyond (16384 x 2048:
+    // 44 us against 49; 16384 x 11008: 436 against 285)
+    const int nc = K <= 256 * 4 * 8 ? 4 : 8;
     int rt = 32;
-    while (rt * kActMaxChunks < K / 8) rt *= 2;
-    switch (rt) {
-#define SBL_CASE(R)                                                                                                       \
-    case R: {                                                                                                             \
-        constexpr int rows = R >= 256 ? 1 : 256 / R;                                                                      \
-        return launch(act_norm_quant_kernel<R, TYPE>, ck.rp / rows, R > 256 ? R : 256, 0, stream, X, T, K, g, eps, Xq, d, \
-                      ck);                                                                                                \
+    while (rt * nc < K / 8) rt *= 2;
+    switch (nc * 10000 + rt) {
+#define SBL_CASE(R, C)                                                                                              \
+    case C * 10000 + R: {                                                                                           \
+        constexpr int rows = R >= 256 ? 1 : 256 / R;                                                                \
+        return launch(act_norm_quant_kernel<R, TYPE, C>, ck.rp / rows, R > 256 ? R : 256, 0, stream, X, T, K, g,    \
+                      eps, Xq, d, ck);                                                                              \
     }
-        SBL_CASE(32)
-        SBL_CASE(64)
-        SBL_CASE(128)
-        SBL_CASE(256)
-        SBL_CASE(512)
-        SBL_CASE(1024)
+        SBL_CASE(32, 4)
+        SBL_CASE(64, 4)
+        SBL_CASE(128, 4)
+        SBL_CASE(256, 4)
+        SBL_CASE(256, 8)
+        SBL_CASE(512, 8)
+        SBL_CASE(1024, 8)
 #undef SBL_CASE
     }
     return SBL_ERR_SHAPE;
 }
 
-// Threads that share a row in the backward: two 8-element chunks each (more
-// for rows longer than 1024 threads hold so).
+// Threads that share a row in the backward: two 8-element chunks each (rows
+// over 8192: see norm_backward).
 static int norm_row_threads(int32_t K)
 {
     int rt = 32;
@@ -510,6 +513,8 @@ static int64_t norm_grid(int32_t T, int32_t K, int num_sms)
 template <int TYPE>
 static sbl_status norm_backward(const NormBwdArgs &a, int64_t grid, cudaStream_t stream)
 {
+    // Longer rows do not leave registers for the next row's loads and spill: 16384 x 11008
+    // runs at 2.3 TB/s where 16384 x 2048 reaches 4.9.
     const int rt = norm_row_threads(a.K);
     const size_t smem = rt < 256 && a.partial ? static_cast<size_t>(a.K) * 4 : 0;
     switch (rt) {
@@ -519,8 +524,9 @@ static sbl_status norm_backward(const NormBwdArgs &a, int64_t grid, cudaStream_t
     case 256: return launch(norm_backward_kernel<TYPE, 256, 2, true>, grid, 256, smem, stream, a);
     case 512: return launch(norm_backward_kernel<TYPE, 512, 2, true>, grid, 512, smem, stream, a);
     default:
-        return a.K <= 1024 * 2 * 8 ? launch(norm_backward_kernel<TYPE, 1024, 2, false>, grid, 1024, smem, stream, a)
-                                   : launch(norm_backward_kernel<TYPE, 1024, 8, false>, grid, 1024, smem, stream, a);
+        return a.K <= 512 * 4 * 8    ? launch(norm_backward_kernel<TYPE, 512, 4, false>, grid, 512, smem, stream, a)
+               : a.K <= 1024 * 2 * 8 ? launch(norm_backward_kernel<TYPE, 1024, 2, false>, grid, 1024, smem, stream, a)
+                                     : launch(norm_backward_kernel<TYPE, 1024, 8, false>, grid, 1024, smem, stream, a);
     }
 }
 
@@ -655,12 +661,12 @@ sbl_status sbl_b8_linear_forward(const sbl_b8_desc *w_desc, const sbl_b8 *w, con
     if ((st = b8_device(&hd)) != SBL_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // One launch that quantises X itself while each CTA's share of it is
-    // small: 64 (token, block) pairs measured even with two launches
-    // (6912 x 2560: 1 token 7.2 us against 8.9, 13 tokens 9.4 against 9.5;
-    // 2560 x 6912: 8 tokens, 56 pairs, 8.9 against 10.1, 13 tokens 10.8 against 10.3).
+    // small: about 112 (token, block) pairs measured even with two launches
+    // (6912 x 2560: 1 token 7.3 us against 9.1, 16 tokens, 80 pairs, 8.5 against 9.8,
+    // 24 tokens 10.4 against 10.2; 2560 x 6912: 16 tokens, 112 pairs, 9.6 against 10.6).
     if (T <= 64) {
         const SkinnyPlan p = skinny_plan(hd.num_sms, w_desc->rows, w_desc->cols, T, true);
-        if (p.smem <= kB8SmemAll && static_cast<int64_t>(T) * p.max_blocks <= 64 && !(y_is_fp32 && p.max_blocks > kB8SegBlocks))
+        if (p.smem <= kB8SmemAll && static_cast<int64_t>(T) * p.max_blocks <= 112 && !(y_is_fp32 && p.max_blocks > kB8SegBlocks))
             return skinny(hd, p, w_desc, w, &xd, X, ldx, xq, Y, ldy, y_is_fp32 != 0, false, false, s);
     }
     if ((st = quantize(hd, &xd, X, false, ldx, false, xq, nullptr, s)) != SBL_OK) return st;

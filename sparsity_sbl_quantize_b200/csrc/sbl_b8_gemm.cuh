@@ -54,11 +54,7 @@ constexpr int kB8SfBufs = 2;
 constexpr int kB8EpiBufBytes = 32 * 64;
 constexpr int kB8EpiBytes = kEpiWarps * kB8EpiBufBytes;
 
-// A kernel that takes c of the 512 columns of tensor memory takes at least
-// c / 512 of the SM's shared memory too (all of it here).  Then CTAs that fit
-// on an SM together also find their tensor memory, whatever kernels and
-// streams they belong to: an allocation that had to wait for another CTA,
-// while both wait for cluster mates elsewhere, could close a circle.
+// The most shared memory a CTA can have.
 constexpr int kB8SmemAll = 227 * 1024;
 
 template <int BN>

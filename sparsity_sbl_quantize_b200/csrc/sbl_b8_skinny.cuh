@@ -27,9 +27,9 @@
 
 namespace sbl {
 
-constexpr int kSkThreads = 256;
-constexpr int kSkQuantWarps = 6;   // warps 2-7 quantise X
-constexpr int kSkQuantBatch = 8;   // (token, block) pairs a half warp has in flight
+constexpr int kSkThreads = 512;
+constexpr int kSkQuantWarps = 14;  // warps 2-15 quantise X
+constexpr int kSkQuantBatch = 4;   // (token, block) pairs a half warp has in flight
 constexpr int kSkMaxStages = 12;
 constexpr int kSkMaxSplit = 8;     // the portable cluster size
 
@@ -132,7 +132,6 @@ __global__ void __launch_bounds__(kSkThreads)
             tma_load_2d(base + s * kStageBytes, &tmW, (b0 + s) * 128, row0, full_bar(s));
         }
     }
-    // dependents may start only here, when every CTA holds its tensor memory
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -209,7 +208,7 @@ __global__ void __launch_bounds__(kSkThreads)
         if (elected) tc_commit(done_bar);
         __syncwarp();
     } else if constexpr (FUSED) {
-        // ------------------------------------ quantise X's part (warps 2-7)
+        // ------------------------------------ quantise X's part (warps 2-15)
         // a half warp per (token, block), kBatch at a time to have the loads in
         // flight together
         constexpr int kHalves = 2 * kSkQuantWarps, kBatch = kSkQuantBatch;
@@ -287,6 +286,13 @@ __global__ void __launch_bounds__(kSkThreads)
         tc_fence_before();
     }
     __syncthreads();
+    // Tensor memory goes back before this CTA waits for its peers: no CTA ever
+    // holds some while it waits for another one, whose allocation might be
+    // waiting for it.
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, args.tmem_cols);
+    }
     if (S > 1) cluster_sync_all();
     // this CTA's rows [r0, r0 + 128 / S) of every token, four rows a thread,
     // every part's load in flight before the first is added
@@ -316,15 +322,7 @@ __global__ void __launch_bounds__(kSkThreads)
                 make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
         }
     }
-    if (S > 1)
-        cluster_sync_all();  // no CTA leaves while a peer reads its sums
-    else
-        __syncthreads();
-    if (warp == 1) {
-        __syncwarp();
-        tc_fence_after();
-        tmem_dealloc(tmem_base, args.tmem_cols);
-    }
+    if (S > 1) cluster_sync_all();  // no CTA leaves while a peer reads its sums
 }
 
 }  // namespace sbl
