@@ -87,8 +87,12 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 3)
     const int sub = threadIdx.x / RT, lt = threadIdx.x % RT;
     const int wr = lt >> 5, lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerCta + sub;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if constexpr (CK == kNoCkpt) {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    } else {
+        grid_wait_and_release();
+    }
     const bool active = row < T;
     const int chunks = K / 8;
 

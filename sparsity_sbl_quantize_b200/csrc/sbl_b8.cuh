@@ -3,6 +3,7 @@
 #pragma once
 
 #include "sbl_b8_format.cuh"
+#include "sbl_device.cuh"
 
 namespace sbl {
 
@@ -25,10 +26,7 @@ struct B8RowArgs {
 template <int TYPE, int SRC>
 __global__ void __launch_bounds__(256) b8_quantize_rows_kernel(B8RowArgs a)
 {
-    // in this order: a kernel launched after this one may read, before its own
-    // wait, whatever was final when this one began (the product reads W)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_wait_and_release();
     const int lane = threadIdx.x & 31, half = lane >> 4;
     const B8Walk u = b8_walk(a.words, a.per_warp);
     if (u.row >= a.rp) return;
@@ -105,8 +103,7 @@ struct B8ReadArgs {
 template <int TYPE>
 __global__ void __launch_bounds__(256) b8_dequantize_kernel(B8ReadArgs a)
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait_and_release();
     const int lane = threadIdx.x & 31, half = lane >> 4;
     const B8Walk u = b8_walk(a.words, a.per_warp);
     if (u.row >= a.rows) return;
@@ -154,6 +151,7 @@ struct B8TileArgs {
     uint32_t *scales_t;
     int64_t rpt;        // cols padded to 128
     int32_t tiles_c;    // column tiles; the grid runs over tiles, columns fastest
+    int32_t late;       // nothing here depends on the kernel before (sbl_device.cuh)
 };
 
 template <int TYPE, int SRC, int SRC_TYPE, bool TILES>
@@ -165,8 +163,7 @@ __global__ void __launch_bounds__(256, SRC == kSrcF32 ? 2 : 4) b8_tile_kernel(B8
     __shared__ __align__(16) uint32_t colmax[16][kMaxWords];
     __shared__ uint32_t wmax[8];
     __shared__ __align__(16) uint8_t rbyte[128], cbyte[128];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!a.late) grid_wait_and_release();
     const int tid = threadIdx.x, lane = tid & 31;
     const int rg = tid >> 4, cg = tid & 15;
     const int tr = static_cast<int>(blockIdx.x) / a.tiles_c;
@@ -175,7 +172,8 @@ __global__ void __launch_bounds__(256, SRC == kSrcF32 ? 2 : 4) b8_tile_kernel(B8
     const bool col_ok = col < a.cols;
     const int row = r0 + 8 * rg;  // the thread's first row
 
-    // the thread's values as they were read
+    // the thread's values as they were read; past L1, which a kernel that has
+    // not waited must not trust (and which has nothing to offer here)
     uint4 q[SRC == kSrcBf16 ? 8 : 1];
     float4 f[SRC == kSrcF32 ? 8 : 1][2];
     uint2 b[SRC == kSrcB8 ? 8 : 1];
@@ -184,7 +182,7 @@ __global__ void __launch_bounds__(256, SRC == kSrcF32 ? 2 : 4) b8_tile_kernel(B8
         const int blk = c0 >> 7;
         if (tid < 128)
             rscale[tid] = r0 + tid < a.rows
-                              ? b8_scale(__ldg(reinterpret_cast<const uint8_t *>(a.xs + b8_word_index(blk >> 2, a.xrp, r0 + tid)) + (blk & 3)))
+                              ? b8_scale(__ldcg(reinterpret_cast<const uint8_t *>(a.xs + b8_word_index(blk >> 2, a.xrp, r0 + tid)) + (blk & 3)))
                               : 1.0f;
     }
 #pragma unroll
@@ -192,14 +190,14 @@ __global__ void __launch_bounds__(256, SRC == kSrcF32 ? 2 : 4) b8_tile_kernel(B8
         const bool ok = col_ok && row + i < a.rows;
         const int64_t at = static_cast<int64_t>(row + i) * a.ldx + col;
         if constexpr (SRC == kSrcBf16) {
-            q[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.X) + at)) : make_uint4(0u, 0u, 0u, 0u);
+            q[i] = ok ? __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.X) + at)) : make_uint4(0u, 0u, 0u, 0u);
         } else if constexpr (SRC == kSrcF32) {
             const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.X) + at);
             const float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            f[i][0] = ok ? __ldg(p) : z;
-            f[i][1] = ok ? __ldg(p + 1) : z;
+            f[i][0] = ok ? __ldcg(p) : z;
+            f[i][1] = ok ? __ldcg(p + 1) : z;
         } else {
-            b[i] = ok ? __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.X) + at)) : make_uint2(0u, 0u);
+            b[i] = ok ? __ldcg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.X) + at)) : make_uint2(0u, 0u);
         }
     }
     if constexpr (SRC == kSrcB8) __syncthreads();
@@ -361,6 +359,7 @@ __global__ void __launch_bounds__(256, SRC == kSrcF32 ? 2 : 4) b8_tile_kernel(B8
                 for (int k = (blk & 3) + 1; k < 4; ++k) p[k] = 127;
         }
     }
+    if (a.late) grid_wait_and_release();
 }
 
 }  // namespace sbl

@@ -39,6 +39,7 @@ struct B8GemmArgs {
     int32_t out_fp32;
     int32_t accumulate;  // fp32 output: add to D
     uint32_t idesc;      // instruction descriptor without the scale-factor ids
+    int32_t late;        // nothing here depends on the kernel before (sbl_device.cuh)
     uint32_t *err;
 };
 
@@ -216,8 +217,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!args.late) grid_wait_and_release();
 
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
@@ -504,6 +504,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem_base, kTmemCols);
     }
+    if (args.late) grid_wait_and_release();
 }
 
 }  // namespace sbl

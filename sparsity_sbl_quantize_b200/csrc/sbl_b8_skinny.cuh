@@ -122,9 +122,8 @@ __global__ void __launch_bounds__(kSkThreads)
     const uint64_t pol = l2_evict_first_policy();
     const int early = !FUSED && args.w_early ? min(args.stages, b1 - b0) : 0;
     if (!FUSED && args.w_early && warp == 0 && lane == 0) {
-        // the kernel before this one quantises X and has itself waited for
-        // its predecessor before letting this one start: W is final, and its
-        // loads need not wait for X
+        // the kernel before this one quantises X and writes nothing of W:
+        // W is final (sbl_device.cuh), and its loads need not wait for X
         mbar_arrive_expect_tx(sf_bar, static_cast<uint32_t>(groups) * 1024u);
         for (int g = 0; g < groups; ++g) bulk_load_1d(sfw_base + 512 * g, args.ws + (g0 + g) * args.wrp + row0, 512, sf_bar, pol);
         for (int s = 0; s < early; ++s) {
@@ -132,8 +131,7 @@ __global__ void __launch_bounds__(kSkThreads)
             tma_load_2d(base + s * kStageBytes, &tmW, (b0 + s) * 128, row0, full_bar(s));
         }
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_wait_and_release();
 
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer

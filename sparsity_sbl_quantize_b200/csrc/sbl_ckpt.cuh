@@ -81,8 +81,7 @@ struct GluFwdArgs {
 template <int TYPE, int ACT, bool GATED>
 __global__ void __launch_bounds__(256) glu_forward_kernel(GluFwdArgs a)
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait_and_release();
     const int lane = threadIdx.x & 31, half = lane >> 4;
     const B8Walk wk = b8_walk(a.words, a.per_warp);
     if (wk.row >= a.rp) return;
@@ -157,8 +156,7 @@ struct GluBwdArgs {
 template <int TYPE, int ACT, bool GATED>
 __global__ void __launch_bounds__(256) glu_backward_kernel(GluBwdArgs a)
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait_and_release();
     const int lane = threadIdx.x & 31, half = lane >> 4;
     const B8Walk wk = b8_walk(a.words, a.per_warp);
     if (wk.row >= a.rows) return;
@@ -230,8 +228,7 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 2) norm_ba
     constexpr int W = RT / 32;
     __shared__ float2 red[2][kRows][W];
     extern __shared__ float dg_sh[];  // [K]
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait_and_release();
     const int sub = threadIdx.x / RT, lt = threadIdx.x % RT;
     const int chunks = a.K / 8;
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
@@ -369,8 +366,7 @@ __global__ void __launch_bounds__(1024) norm_dgain_kernel(const float *__restric
                                                           float *__restrict__ dgain)
 {
     __shared__ float sh[32][33];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait_and_release();
     const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
     const int k = blockIdx.x * 32 + lane;
     float s = 0.0f;

@@ -109,6 +109,18 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// --------------------------------------------- programmatic dependent launch --
+// Kernels that use these let their dependents start only after their own
+// wait, so when a kernel starts, everything before its predecessor is complete
+// and visible.  One that needs nothing from its predecessor itself may
+// therefore work at once and wait at its end instead (`late`), where the wait
+// keeps that promise for the kernel after it.
+__device__ __forceinline__ void grid_wait_and_release()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // -------------------------------------------------------------------- TMA --
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map)
 {

@@ -414,7 +414,7 @@ def b8_desc(rows: int, cols: int, type: int = SBL_B8_E4M3) -> sbl_b8_desc:
 
 
 def _b8ref(m: Optional[Block8]):
-    return ctypes.byref(m.c()) if m is not None else None
+    return None if m is None else sbl_b8(m.codes.data_ptr(), m.scales.data_ptr())
 
 
 def _ld(t: Optional[torch.Tensor]) -> int:
@@ -424,7 +424,9 @@ def _ld(t: Optional[torch.Tensor]) -> int:
     s = t.stride()
     if len(s) != 2 or s[1] != 1:
         raise ValueError("a 2-D tensor with contiguous rows is needed")
-    return s[0] if t.shape[0] > 1 else t.shape[1]
+    if s[0] > 1:
+        return s[0]
+    return t.size(1) if t.size(0) == 1 else s[0]  # one row has no stride; overlapping rows the library refuses
 
 
 def _fp32(t: Optional[torch.Tensor]) -> int:
@@ -432,11 +434,11 @@ def _fp32(t: Optional[torch.Tensor]) -> int:
 
 
 def sbl_b8_row_bytes(d: sbl_b8_desc) -> int:
-    return int(_lib.sbl_b8_row_bytes(ctypes.byref(d)))
+    return int(_lib.sbl_b8_row_bytes(d))
 
 
 def sbl_b8_scale_bytes(d: sbl_b8_desc) -> int:
-    return int(_lib.sbl_b8_scale_bytes(ctypes.byref(d)))
+    return int(_lib.sbl_b8_scale_bytes(d))
 
 
 def alloc_b8(d: sbl_b8_desc, device="cuda") -> Block8:
@@ -448,34 +450,34 @@ def alloc_b8(d: sbl_b8_desc, device="cuda") -> Block8:
 def sbl_b8_quantize(d: sbl_b8_desc, X: torch.Tensor, out: Optional[Block8], out_t: Optional[Block8] = None,
                     blocks: int = SBL_B8_ROWS) -> None:
     """X (bf16 or fp32, any row stride) -> out and / or its transpose out_t."""
-    _check(_lib.sbl_b8_quantize(ctypes.byref(d), _ptr(X), _fp32(X), _ld(X), blocks, _b8ref(out), _b8ref(out_t),
-                                _stream()), "sbl_b8_quantize")
+    _check(_lib.sbl_b8_quantize(d, _ptr(X), _fp32(X), _ld(X), blocks, _b8ref(out), _b8ref(out_t), _stream()),
+           "sbl_b8_quantize")
 
 
 def sbl_b8_transpose(d: sbl_b8_desc, src: Block8, out_t: Block8, type_t: Optional[int] = None) -> None:
-    _check(_lib.sbl_b8_transpose(ctypes.byref(d), _b8ref(src), d.type if type_t is None else type_t, _b8ref(out_t),
+    _check(_lib.sbl_b8_transpose(d, _b8ref(src), d.type if type_t is None else type_t, _b8ref(out_t),
                                  _stream()), "sbl_b8_transpose")
 
 
 def sbl_b8_dequantize(d: sbl_b8_desc, src: Block8, X: torch.Tensor) -> None:
-    _check(_lib.sbl_b8_dequantize(ctypes.byref(d), _b8ref(src), _ptr(X), _ld(X), _stream()), "sbl_b8_dequantize")
+    _check(_lib.sbl_b8_dequantize(d, _b8ref(src), _ptr(X), _ld(X), _stream()), "sbl_b8_dequantize")
 
 
 def sbl_b8_gemm(ad: sbl_b8_desc, a: Block8, bd: sbl_b8_desc, b: Block8, D: torch.Tensor, accumulate: bool = False) -> None:
     """D [a rows, b rows] (bf16 or fp32) = or += a b^T."""
-    _check(_lib.sbl_b8_gemm(ctypes.byref(ad), _b8ref(a), ctypes.byref(bd), _b8ref(b), _ptr(D), _ld(D), _fp32(D),
+    _check(_lib.sbl_b8_gemm(ad, _b8ref(a), bd, _b8ref(b), _ptr(D), _ld(D), _fp32(D),
                             1 if accumulate else 0, _stream()), "sbl_b8_gemm")
 
 
 def sbl_b8_linear_forward(wd: sbl_b8_desc, w: Block8, X: torch.Tensor, T: int, xq: Block8, Y: torch.Tensor,
                           x_type: int = SBL_B8_E4M3) -> None:
     """X (bf16) -> its 8-bit form xq (the backward's checkpoint) and Y = xq w^T (bf16 or fp32)."""
-    _check(_lib.sbl_b8_linear_forward(ctypes.byref(wd), _b8ref(w), _ptr(X), _ld(X), T, x_type, _b8ref(xq), _ptr(Y),
+    _check(_lib.sbl_b8_linear_forward(wd, _b8ref(w), _ptr(X), _ld(X), T, x_type, _b8ref(xq), _ptr(Y),
                                       _ld(Y), _fp32(Y), _stream()), "sbl_b8_linear_forward")
 
 
 def sbl_b8_linear_workspace_bytes(wd: sbl_b8_desc, T: int) -> int:
-    return int(_lib.sbl_b8_linear_workspace_bytes(ctypes.byref(wd), T))
+    return int(_lib.sbl_b8_linear_workspace_bytes(wd, T))
 
 
 def sbl_b8_linear_backward(wd: sbl_b8_desc, w_t: Optional[Block8], xq: Optional[Block8], dY: torch.Tensor, T: int,
@@ -483,7 +485,7 @@ def sbl_b8_linear_backward(wd: sbl_b8_desc, w_t: Optional[Block8], xq: Optional[
                            x_type: int = SBL_B8_E4M3, g_type: int = SBL_B8_E4M3, accumulate: bool = False) -> None:
     """dX (bf16 or fp32) and dW (fp32, added to when accumulate) from the checkpoint xq."""
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.sbl_b8_linear_backward(ctypes.byref(wd), _b8ref(w_t), _b8ref(xq), x_type, _ptr(dY), _ld(dY), T, g_type,
+    _check(_lib.sbl_b8_linear_backward(wd, _b8ref(w_t), _b8ref(xq), x_type, _ptr(dY), _ld(dY), T, g_type,
                                        _ptr(dX), _fp32(dX), _ptr(dW), 1 if accumulate else 0, _ptr(workspace), nbytes,
                                        _stream()), "sbl_b8_linear_backward")
 
@@ -491,19 +493,19 @@ def sbl_b8_linear_backward(wd: sbl_b8_desc, w_t: Optional[Block8], xq: Optional[
 def sbl_glu_forward(d: sbl_b8_desc, act: int, G: torch.Tensor, U: Optional[torch.Tensor], H: Optional[torch.Tensor],
                     g8: Optional[Block8] = None, u8: Optional[Block8] = None) -> None:
     """H = act(G) * U and the checkpoints of G and U; every output optional."""
-    _check(_lib.sbl_glu_forward(ctypes.byref(d), act, _ptr(G), _ld(G), _ptr(U), _ld(U), _ptr(H), _ld(H), _b8ref(g8),
+    _check(_lib.sbl_glu_forward(d, act, _ptr(G), _ld(G), _ptr(U), _ld(U), _ptr(H), _ld(H), _b8ref(g8),
                                 _b8ref(u8), _stream()), "sbl_glu_forward")
 
 
 def sbl_glu_backward(d: sbl_b8_desc, act: int, g8: Block8, u8: Optional[Block8], dH: torch.Tensor, dG: torch.Tensor,
                      dU: Optional[torch.Tensor]) -> None:
-    _check(_lib.sbl_glu_backward(ctypes.byref(d), act, _b8ref(g8), _b8ref(u8), _ptr(dH), _ld(dH), _ptr(dG), _ld(dG),
+    _check(_lib.sbl_glu_backward(d, act, _b8ref(g8), _b8ref(u8), _ptr(dH), _ld(dH), _ptr(dG), _ld(dG),
                                  _ptr(dU), _ld(dU), _stream()), "sbl_glu_backward")
 
 
 def sbl_quantize_act_rmsnorm_checkpoint(d: sbl_b8_desc, X: torch.Tensor, g: Optional[torch.Tensor], eps: float,
                                         Xq: torch.Tensor, dscale: torch.Tensor, x8: Block8) -> None:
-    _check(_lib.sbl_quantize_act_rmsnorm_checkpoint(ctypes.byref(d), _ptr(X), _ptr(g), float(eps), _ptr(Xq), _ptr(dscale),
+    _check(_lib.sbl_quantize_act_rmsnorm_checkpoint(d, _ptr(X), _ptr(g), float(eps), _ptr(Xq), _ptr(dscale),
                                                     _b8ref(x8), _stream()), "sbl_quantize_act_rmsnorm_checkpoint")
 
 
@@ -516,7 +518,7 @@ def sbl_rmsnorm_backward(d: sbl_b8_desc, x8: Block8, g: Optional[torch.Tensor], 
                          workspace: Optional[torch.Tensor]) -> None:
     """dX (+ dR) and the gains' gradient dg from the checkpointed norm input x8."""
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.sbl_rmsnorm_backward(ctypes.byref(d), _b8ref(x8), _ptr(g), float(eps), _ptr(dU), _ptr(dR), _ptr(dX),
+    _check(_lib.sbl_rmsnorm_backward(d, _b8ref(x8), _ptr(g), float(eps), _ptr(dU), _ptr(dR), _ptr(dX),
                                      _ptr(dg), _ptr(workspace), nbytes, _stream()), "sbl_rmsnorm_backward")
 
 
