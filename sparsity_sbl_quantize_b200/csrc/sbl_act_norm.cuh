@@ -3,7 +3,7 @@
 #pragma once
 
 #include "sbl_b8_format.cuh"
-#include "sbl_device.cuh"
+#include "sbl_b8_device.cuh"
 
 namespace sbl {
 

@@ -3,7 +3,7 @@
 #pragma once
 
 #include "sbl_b8_format.cuh"
-#include "sbl_device.cuh"
+#include "sbl_b8_device.cuh"
 
 namespace sbl {
 
@@ -151,7 +151,7 @@ struct B8TileArgs {
     uint32_t *scales_t;
     int64_t rpt;        // cols padded to 128
     int32_t tiles_c;    // column tiles; the grid runs over tiles, columns fastest
-    int32_t late;       // nothing here depends on the kernel before (sbl_device.cuh)
+    int32_t late;       // nothing here depends on the kernel before (sbl_b8_device.cuh)
 };
 
 template <int TYPE, int SRC, int SRC_TYPE, bool TILES>

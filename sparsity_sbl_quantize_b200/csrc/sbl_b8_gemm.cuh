@@ -27,7 +27,7 @@
 #include <cuda_bf16.h>
 
 #include "sbl_b8_format.cuh"
-#include "sbl_device.cuh"
+#include "sbl_b8_device.cuh"
 #include "sbl_gemm.cuh"  // tile raster, role sizes
 
 namespace sbl {
@@ -39,7 +39,7 @@ struct B8GemmArgs {
     int32_t out_fp32;
     int32_t accumulate;  // fp32 output: add to D
     uint32_t idesc;      // instruction descriptor without the scale-factor ids
-    int32_t late;        // nothing here depends on the kernel before (sbl_device.cuh)
+    int32_t late;        // nothing here depends on the kernel before (sbl_b8_device.cuh)
     uint32_t *err;
 };
 

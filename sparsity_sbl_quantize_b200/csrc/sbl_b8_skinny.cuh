@@ -23,7 +23,7 @@
 
 #include "sbl_b8.cuh"
 #include "sbl_b8_gemm.cuh"
-#include "sbl_device.cuh"
+#include "sbl_b8_device.cuh"
 
 namespace sbl {
 
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kSkThreads)
     const int early = !FUSED && args.w_early ? min(args.stages, b1 - b0) : 0;
     if (!FUSED && args.w_early && warp == 0 && lane == 0) {
         // the kernel before this one quantises X and writes nothing of W:
-        // W is final (sbl_device.cuh), and its loads need not wait for X
+        // W is final (sbl_b8_device.cuh), and its loads need not wait for X
         mbar_arrive_expect_tx(sf_bar, static_cast<uint32_t>(groups) * 1024u);
         for (int g = 0; g < groups; ++g) bulk_load_1d(sfw_base + 512 * g, args.ws + (g0 + g) * args.wrp + row0, 512, sf_bar, pol);
         for (int s = 0; s < early; ++s) {

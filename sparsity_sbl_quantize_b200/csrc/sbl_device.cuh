@@ -18,7 +18,6 @@ enum : uint32_t {
     kErrDecode = 1u << 3,
     kErrPack = 1u << 4,
     kErrGemv = 1u << 5,
-    kErrB8Gemm = 1u << 6,
 };
 
 // Every device-side wait gives up after this long and records an error.
@@ -85,40 +84,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_
             return false;
         }
     }
-}
-
-// The same, reading the clock only after some tries: a read of the global
-// timer takes longer than most waits of a single issuing thread.
-__device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, uint32_t *err, uint32_t code)
-{
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait(bar, parity, err, code);
-}
-
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(p));
-    return p != 0;
-}
-
-// --------------------------------------------- programmatic dependent launch --
-// Kernels that use these let their dependents start only after their own
-// wait, so when a kernel starts, everything before its predecessor is complete
-// and visible.  One that needs nothing from its predecessor itself may
-// therefore work at once and wait at its end instead (`late`), where the wait
-// keeps that promise for the kernel after it.
-__device__ __forceinline__ void grid_wait_and_release()
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // -------------------------------------------------------------------- TMA --
