@@ -465,3 +465,23 @@ def test_results_do_not_depend_on_the_run():
         sbl.sbl_rmsnorm_backward(d, x8, g, 1e-5, du, None, dx, dg, ws)
         got.append((dx, dg))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("spread", [0, 3, 5, 6, 12, 40])
+@pytest.mark.parametrize("rows,cols", [(128, 128), (200, 272)])
+def test_transpose_of_scales_near_and_far_apart(spread, rows, cols):
+    """e4m3 to e4m3 over rows whose scales differ by up to 2^spread, columns far below the rest and empty ones."""
+    sbl = sbl_mod()
+    r = rng(spread, rows, 20)
+    x = r.standard_normal((rows, cols)) * np.exp2(r.integers(-spread, 1, (rows, 1)))
+    x[:, 5] *= 2.0 ** -7
+    x[:, 9] *= 2.0 ** -12
+    x[:, 11] *= 2.0 ** -16
+    x[:, 17] = 0
+    x[:, 40:44] = 448.0 * np.exp2(r.integers(-10, 1, (rows, 4)))
+    t, v = bf16(x)
+    d, m = new(sbl, rows, cols, ref.E4M3)
+    _, mt = new(sbl, cols, rows, ref.E4M3)
+    sbl.sbl_b8_quantize(d, t, m)
+    sbl.sbl_b8_transpose(d, m, mt)
+    check_stored(mt, rows, ref.E4M3, *ref.quantize(np.ascontiguousarray(ref.value(v, ref.E4M3).T), ref.E4M3))
