@@ -33,12 +33,12 @@ __global__ void __launch_bounds__(256) b8_quantize_rows_kernel(B8RowArgs a)
     uint32_t *scales = a.scales + b8_word_index(0, a.rp, u.row);
     if (u.row >= a.rows) {
         if (lane == 0)
-            for (int w = u.w0; w < u.w1; ++w) scales[w * a.rp] = kB8PadWord;
+            for (int w = u.w0; w < u.w1; w += u.step) scales[w * a.rp] = kB8PadWord;
         return;
     }
     const int l0 = 128 * half + 8 * (lane & 15);
     uint8_t *codes = a.codes + u.row * a.ldc;
-    for (int w = u.w0; w < u.w1; ++w) {
+    for (int w = u.w0; w < u.w1; w += u.step) {
         uint32_t word = 0;
         const int c0 = 512 * w + l0;
         if constexpr (SRC == kSrcBf16) {
@@ -47,9 +47,10 @@ __global__ void __launch_bounds__(256) b8_quantize_rows_kernel(B8RowArgs a)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 v[i] = c0 + 256 * i < a.cols ? __ldg(reinterpret_cast<const uint4 *>(x + c0 + 256 * i)) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t top = half_warp_max2(bf16x8_absmax(v[0]) | (bf16x8_absmax(v[1]) << 16));
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(bf16x8_absmax(v[i])) << 16);
+                const uint32_t byte = b8_scale_byte<TYPE>(i ? top & 0xffff0000u : top << 16);
                 const uint2 q = b8_encode_bf16x8<TYPE>(v[i], b8_inv_scale(byte));
                 if (c0 + 256 * i < a.cols) *reinterpret_cast<uint2 *>(codes + c0 + 256 * i) = q;
                 word |= byte << (8 * (2 * i + half));
@@ -76,9 +77,7 @@ __global__ void __launch_bounds__(256) b8_quantize_rows_kernel(B8RowArgs a)
                 uint32_t q[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    q[h] = inv == 0.0f ? 0u
-                                       : b8_encode4<TYPE>(__fmul_rn(v[i][h].x, inv), __fmul_rn(v[i][h].y, inv),
-                                                          __fmul_rn(v[i][h].z, inv), __fmul_rn(v[i][h].w, inv));
+                    q[h] = inv == 0.0f ? 0u : b8_scale_encode4<TYPE>(v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w, inv);
                 if (c0 + 256 * i < a.cols) *reinterpret_cast<uint2 *>(codes + c0 + 256 * i) = make_uint2(q[0], q[1]);
                 word |= byte << (8 * (2 * i + half));
             }
@@ -109,7 +108,7 @@ __global__ void __launch_bounds__(256) b8_dequantize_kernel(B8ReadArgs a)
     if (u.row >= a.rows) return;
     const uint32_t *scales = a.scales + b8_word_index(0, a.rp, u.row);
     const int l0 = 128 * half + 8 * (lane & 15);
-    for (int w = u.w0; w < u.w1; ++w) {
+    for (int w = u.w0; w < u.w1; w += u.step) {
         const int c0 = 512 * w + l0;
         const uint32_t word = __ldg(scales + w * a.rp);
 #pragma unroll

@@ -96,6 +96,11 @@ static int32_t words_per_warp(int64_t rows, int32_t words, int num_sms)
 template <typename Args>
 static sbl_status launch_walk(const HostDevice &hd, void (*kernel)(Args), int64_t rows, Args a, cudaStream_t stream)
 {
+    // many long rows: a CTA a row (gated backward of 16384 x 11008 from e4m3 checkpoints 231 -> 214 us)
+    if (a.words >= 8 && rows >= 8ll * hd.num_sms) {
+        a.per_warp = 0;
+        return launch2(kernel, rows, 1, 256, 0, stream, a);
+    }
     a.per_warp = words_per_warp(rows, a.words, hd.num_sms);
     return launch2(kernel, (rows + 7) / 8, (a.words + a.per_warp - 1) / a.per_warp, 256, 0, stream, a);
 }
@@ -418,7 +423,8 @@ static sbl_status gemm(const HostDevice &hd, const sbl_b8_desc *ad, const sbl_b8
     const int64_t tiles_w = (args.N + kBM - 1) / kBM;
     if (args.M <= 64 || (args.M <= 128 && 4 * tiles_w <= hd.num_sms)) {
         const SkinnyPlan p = skinny_plan(hd.num_sms, bd->rows, bd->cols, ad->rows, false);
-        if (!fp32 || p.max_blocks <= kB8SegBlocks)  // longer fp32 sums: see LONG
+        // not for fp32 sums that need LONG, nor for a K whose scales do not fit
+        if ((!fp32 || p.max_blocks <= kB8SegBlocks) && p.smem <= kB8SmemAll && p.tmem_cols <= kTmemCols)
             return skinny(hd, p, bd, B, ad, nullptr, 0, A, D, ldd, fp32, accumulate, w_early, stream);
     }
     // 128 x 256 tiles or 128 x 128 ones, of which a product with few tiles has
@@ -670,7 +676,7 @@ sbl_status sbl_b8_linear_forward(const sbl_b8_desc *w_desc, const sbl_b8 *w, con
     // 24 tokens 10.4 against 10.2; 2560 x 6912: 16 tokens, 112 pairs, 9.6 against 10.6).
     if (T <= 64) {
         const SkinnyPlan p = skinny_plan(hd.num_sms, w_desc->rows, w_desc->cols, T, true);
-        if (p.smem <= kB8SmemAll && static_cast<int64_t>(T) * p.max_blocks <= 112 && !(y_is_fp32 && p.max_blocks > kB8SegBlocks))
+        if (p.smem <= kB8SmemAll && p.tmem_cols <= kTmemCols && static_cast<int64_t>(T) * p.max_blocks <= 112 && !(y_is_fp32 && p.max_blocks > kB8SegBlocks))
             return skinny(hd, p, w_desc, w, &xd, X, ldx, xq, Y, ldy, y_is_fp32 != 0, false, false, s);
     }
     if ((st = quantize(hd, &xd, X, false, ldx, false, xq, nullptr, s)) != SBL_OK) return st;

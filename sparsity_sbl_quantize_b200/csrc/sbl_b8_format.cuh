@@ -93,6 +93,21 @@ __device__ __forceinline__ uint32_t b8_encode4(float a, float b, float c, float 
     }
 }
 
+// Four codes of values still to be scaled by inv = 2^-e.  int8: the product
+// is exact, so it may be fused with the rounding addition.
+template <int TYPE>
+__device__ __forceinline__ uint32_t b8_scale_encode4(float a, float b, float c, float d, float inv)
+{
+    if constexpr (TYPE == kB8I8) {
+        const float m = 12582912.0f;  // see rne_byte
+        const uint32_t q0 = __float_as_uint(__fmaf_rn(a, inv, m)), q1 = __float_as_uint(__fmaf_rn(b, inv, m));
+        const uint32_t q2 = __float_as_uint(__fmaf_rn(c, inv, m)), q3 = __float_as_uint(__fmaf_rn(d, inv, m));
+        return __byte_perm(__byte_perm(q0, q1, 0x0040), __byte_perm(q2, q3, 0x0040), 0x5410);
+    } else {
+        return b8_encode4<TYPE>(__fmul_rn(a, inv), __fmul_rn(b, inv), __fmul_rn(c, inv), __fmul_rn(d, inv));
+    }
+}
+
 // The values (unscaled) of the four codes of a word.
 template <int TYPE>
 __device__ __forceinline__ void b8_decode4(uint32_t w, float (&v)[4])
@@ -122,25 +137,35 @@ __device__ __forceinline__ uint32_t bf16x8_absmax(const uint4 &v)
 template <int TYPE>
 __device__ __forceinline__ uint2 b8_encode_bf16x8(const uint4 &v, float inv)
 {
-    const uint2 w = make_uint2(b8_encode4<TYPE>(__fmul_rn(bf16_lo(v.x), inv), __fmul_rn(bf16_hi(v.x), inv),
-                                                __fmul_rn(bf16_lo(v.y), inv), __fmul_rn(bf16_hi(v.y), inv)),
-                               b8_encode4<TYPE>(__fmul_rn(bf16_lo(v.z), inv), __fmul_rn(bf16_hi(v.z), inv),
-                                                __fmul_rn(bf16_lo(v.w), inv), __fmul_rn(bf16_hi(v.w), inv)));
+    const uint2 w = make_uint2(b8_scale_encode4<TYPE>(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y), inv),
+                               b8_scale_encode4<TYPE>(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w), inv));
     return inv == 0.0f ? make_uint2(0u, 0u) : w;
 }
 
-// How the element-wise kernels walk a matrix: warp v of a CTA takes row
-// 8 blockIdx.x + v and the scale words [w0, w1) of it (512 columns each); no
-// division, and a few words a warp amortise the row's addresses.
+// How the element-wise kernels walk a matrix (no division: a 64-bit one costs
+// as much as the work on six elements).  per_warp > 0: warp v of a CTA takes row
+// 8 blockIdx.x + v and the scale words [w0, w1) of it (512 columns each).
+// per_warp == 0, for rows of many words: the CTA takes row blockIdx.x, its warps
+// the words v, v + 8, ..., so that it streams through one stretch of memory.
 struct B8Walk {
     int64_t row;
-    int w0, w1;
+    int w0, w1, step;
 };
 
 __device__ __forceinline__ B8Walk b8_walk(int words, int per_warp)
 {
+    const int v = threadIdx.x >> 5;
+    if (per_warp == 0) return {static_cast<int64_t>(blockIdx.x), v, words, 8};
     const int w0 = static_cast<int>(blockIdx.y) * per_warp;
-    return {static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5), w0, min(w0 + per_warp, words)};
+    return {static_cast<int64_t>(blockIdx.x) * 8 + v, w0, min(w0 + per_warp, words), 1};
+}
+
+// max over the 16 lanes of a half warp, of two 16-bit magnitudes at once
+__device__ __forceinline__ uint32_t half_warp_max2(uint32_t v)
+{
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) v = __vmaxu2(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
 }
 
 // max over the 16 lanes of a half warp

@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(256) glu_forward_kernel(GluFwdArgs a)
     const int64_t wi = b8_word_index(0, a.rp, wk.row);
     if (wk.row >= a.rows) {
         if (lane == 0)
-            for (int w = wk.w0; w < wk.w1; ++w) {
+            for (int w = wk.w0; w < wk.w1; w += wk.step) {
                 if (a.gc) a.gs[wi + w * a.rp] = kB8PadWord;
                 if (GATED && a.uc) a.us[wi + w * a.rp] = kB8PadWord;
             }
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(256) glu_forward_kernel(GluFwdArgs a)
     const int l0 = 128 * half + 8 * (lane & 15);
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
     const uint16_t *G = a.G + wk.row * a.ldg, *U = GATED ? a.U + wk.row * a.ldu : nullptr;
-    for (int w = wk.w0; w < wk.w1; ++w) {
+    for (int w = wk.w0; w < wk.w1; w += wk.step) {
         const int c0 = 512 * w + l0;
         uint4 g[2], u[2];
 #pragma unroll
@@ -119,13 +119,15 @@ __global__ void __launch_bounds__(256) glu_forward_kernel(GluFwdArgs a)
                 for (int k = 0; k < 8; ++k) h[k] = GATED ? act_value<ACT>(gv[k]) * uv[k] : act_value<ACT>(gv[k]);
                 *reinterpret_cast<uint4 *>(a.H + wk.row * a.ldh + c) = pack_bf16x8(h);
             }
+            // the largest magnitudes of both blocks in one reduction
+            const uint32_t top = half_warp_max2(bf16x8_absmax(g[i]) | (GATED ? bf16x8_absmax(u[i]) << 16 : 0u));
             if (a.gc) {
-                const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(bf16x8_absmax(g[i])) << 16);
+                const uint32_t byte = b8_scale_byte<TYPE>(top << 16);
                 if (ok) *reinterpret_cast<uint2 *>(a.gc + wk.row * a.ldc + c) = b8_encode_bf16x8<TYPE>(g[i], b8_inv_scale(byte));
                 gw |= byte << (8 * (2 * i + half));
             }
             if (GATED && a.uc) {
-                const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(bf16x8_absmax(u[i])) << 16);
+                const uint32_t byte = b8_scale_byte<TYPE>(top & 0xffff0000u);
                 if (ok) *reinterpret_cast<uint2 *>(a.uc + wk.row * a.ldc + c) = b8_encode_bf16x8<TYPE>(u[i], b8_inv_scale(byte));
                 uw |= byte << (8 * (2 * i + half));
             }
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(256) glu_backward_kernel(GluBwdArgs a)
     if (wk.row >= a.rows) return;
     const int64_t wi = b8_word_index(0, a.rp, wk.row);
     const int l0 = 128 * half + 8 * (lane & 15);
-    for (int w = wk.w0; w < wk.w1; ++w) {
+    for (int w = wk.w0; w < wk.w1; w += wk.step) {
         const int c0 = 512 * w + l0;
         const uint32_t gw = __ldg(a.gs + wi + w * a.rp), uw = GATED ? __ldg(a.us + wi + w * a.rp) : 0u;
         uint2 gq[2], uq[2];

@@ -485,3 +485,72 @@ def test_transpose_of_scales_near_and_far_apart(spread, rows, cols):
     sbl.sbl_b8_quantize(d, t, m)
     sbl.sbl_b8_transpose(d, m, mt)
     check_stored(mt, rows, ref.E4M3, *ref.quantize(np.ascontiguousarray(ref.value(v, ref.E4M3).T), ref.E4M3))
+
+
+@pytest.mark.parametrize("m,n,fp32", [(16, 16, False), (64, 48, True), (80, 32, False)])
+def test_gemm_over_a_very_long_k(m, n, fp32):
+    """A reduction whose scales no longer fit beside the few-row kernel's accumulators."""
+    sbl = sbl_mod()
+    k = 250_000
+    ad, a, av = operands(sbl, rng(m, n, 21), m, k, ref.E4M3)
+    bd, b, bv = operands(sbl, rng(m, n, 22), n, k, ref.E4M3)
+    out = torch.empty((m, n), dtype=torch.float32 if fp32 else torch.bfloat16, device="cuda")
+    sbl.sbl_b8_gemm(ad, a, bd, b, out)
+    check_product(out.double().cpu().numpy(), av, bv, ref.HALF["fp32" if fp32 else "bf16"])
+
+
+class Guarded:
+    """A tensor between two guard bands of 512 bytes."""
+
+    def __init__(self, *shape, dtype=torch.uint8):
+        n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+        self.raw = torch.full((1024 + -(-n // 512) * 512,), 0xC3, dtype=torch.uint8, device="cuda")
+        self.n = n
+        self.t = self.raw[512:512 + n].view(dtype).view(*shape)
+
+    def intact(self):
+        return bool((self.raw[:512] == 0xC3).all()) and bool((self.raw[512 + self.n:] == 0xC3).all())
+
+
+@pytest.mark.parametrize("t,k,o", [(1, 16, 16), (13, 400, 272), (130, 1040, 144), (300, 656, 528)])
+def test_nothing_is_written_past_the_outputs(t, k, o):
+    sbl = sbl_mod()
+    r = rng(t, k, o, 23)
+    held = []
+
+    def g(*shape, dtype=torch.uint8):
+        held.append(Guarded(*shape, dtype=dtype))
+        return held[-1].t
+
+    def mat(rows, cols, typ):
+        d = sbl.b8_desc(rows, cols, typ)
+        return d, sbl.Block8(codes=g(rows, sbl.sbl_b8_row_bytes(d)), scales=g(sbl.sbl_b8_scale_bytes(d)))
+
+    bf, f32 = torch.bfloat16, torch.float32
+    (x, _), (dy, _), (u, _) = bf16(r.standard_normal((t, k))), bf16(r.standard_normal((t, o))), bf16(r.standard_normal((t, k)))
+    w = torch.from_numpy(r.standard_normal((o, k)).astype(np.float32)).cuda()
+    wd, wq = mat(o, k, 0)
+    _, wt = mat(k, o, 0)
+    xd, xq = mat(t, k, 0)
+    sbl.sbl_b8_quantize(wd, w, wq, wt, sbl.SBL_B8_TILES)
+    sbl.sbl_b8_linear_forward(wd, wq, x, t, xq, g(t, o, dtype=bf))
+    ws = g(sbl.sbl_b8_linear_workspace_bytes(wd, t))
+    sbl.sbl_b8_linear_backward(wd, wt, xq, dy, t, g(t, k, dtype=bf), g(o, k, dtype=f32), ws)
+    for typ in TYPES:
+        d, m = mat(t, k, typ)
+        _, mt = mat(k, t, typ)
+        sbl.sbl_b8_quantize(d, x, m)
+        sbl.sbl_b8_quantize(d, x, m, mt)
+        sbl.sbl_b8_transpose(d, m, mt)
+        sbl.sbl_b8_dequantize(d, m, g(t, k, dtype=bf))
+        (_, g8), (_, u8) = mat(t, k, typ), mat(t, k, typ)
+        sbl.sbl_glu_forward(d, 0, x, u, g(t, k, dtype=bf), g8, u8)
+        sbl.sbl_glu_backward(d, 0, g8, u8, u, g(t, k, dtype=bf), g(t, k, dtype=bf))
+        _, x8 = mat(t, k, typ)
+        gain = torch.ones(k, dtype=bf, device="cuda")
+        sbl.sbl_quantize_act_rmsnorm_checkpoint(d, x, gain, 1e-5, g(t, k, dtype=torch.int8), g(t, dtype=f32), x8)
+        sbl.sbl_rmsnorm_backward(d, x8, gain, 1e-5, u, None, g(t, k, dtype=bf), g(k, dtype=f32),
+                                 g(sbl.sbl_rmsnorm_backward_workspace_bytes(t, k)))
+    torch.cuda.synchronize()
+    assert all(h.intact() for h in held)
+    assert sbl.sbl_device_error() == 0
