@@ -241,3 +241,16 @@ def test_weights_quantised_right_before_the_product():
             sbl.sbl_b8_linear_forward(wd, w, x, t, xq, y)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(alone, run))
+
+
+@pytest.mark.parametrize("op", ["quantize", "both", "transpose", "linear", "linear_backward", "glu", "glu_backward", "rmsnorm",
+                                "rmsnorm_backward"])
+def test_timing_command(op):
+    import json
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-m", "sparsity_sbl_quantize_b200.run_b8", op, "96", "256", "144", "--iters", "2", "--warmup", "1"],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    line = json.loads(r.stdout)
+    assert line["op"] == op and line["iters"] == 2 and line["ms_per_call"] > 0
