@@ -8,9 +8,11 @@
 namespace sbl {
 
 // ------------------------------------------------------------ row blocks --
-// One warp per (row, 512 columns): lane l of half h holds the eight values at
-// columns 256 i + 128 h + 8 (l % 16), i = 0, 1, so half h of pass i is one
-// block and the warp writes one scale word.  X is read once; memory bound.
+// One warp per (row, 512 columns): lane l holds the sixteen values at columns
+// 16 l .., eight lanes a block, and the warp writes one scale word.  What is done
+// once per block is thus shared by sixteen values a lane (with eight, the
+// int8 gated activation below spent a quarter of its instructions on it).
+// Memory bound: 16384 x 11008 at the copy rate.
 struct B8RowArgs {
     const void *X;
     int64_t ldx;        // elements
@@ -21,13 +23,14 @@ struct B8RowArgs {
     int64_t rp;         // rows padded to 128
     int32_t words;      // scale words per row
     int32_t per_warp;   // of which a warp takes so many
+    int32_t v32;        // bf16 rows are 32-byte aligned
 };
 
 template <int TYPE, int SRC>
 __global__ void __launch_bounds__(256) b8_quantize_rows_kernel(B8RowArgs a)
 {
     grid_wait_and_release();
-    const int lane = threadIdx.x & 31, half = lane >> 4;
+    const int lane = threadIdx.x & 31;
     const B8Walk u = b8_walk(a.words, a.per_warp);
     if (u.row >= a.rp) return;
     uint32_t *scales = a.scales + b8_word_index(0, a.rp, u.row);
@@ -36,53 +39,36 @@ __global__ void __launch_bounds__(256) b8_quantize_rows_kernel(B8RowArgs a)
             for (int w = u.w0; w < u.w1; w += u.step) scales[w * a.rp] = kB8PadWord;
         return;
     }
-    const int l0 = 128 * half + 8 * (lane & 15);
     uint8_t *codes = a.codes + u.row * a.ldc;
     for (int w = u.w0; w < u.w1; w += u.step) {
-        uint32_t word = 0;
-        const int c0 = 512 * w + l0;
+        const int c = 512 * w + 16 * lane;
+        const bool ok = c < a.cols;
+        uint32_t byte;
+        uint4 q;
         if constexpr (SRC == kSrcBf16) {
-            uint4 v[2];
-            const uint16_t *x = static_cast<const uint16_t *>(a.X) + u.row * a.ldx;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                v[i] = c0 + 256 * i < a.cols ? __ldg(reinterpret_cast<const uint4 *>(x + c0 + 256 * i)) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t top = half_warp_max2(bf16x8_absmax(v[0]) | (bf16x8_absmax(v[1]) << 16));
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t byte = b8_scale_byte<TYPE>(i ? top & 0xffff0000u : top << 16);
-                const uint2 q = b8_encode_bf16x8<TYPE>(v[i], b8_inv_scale(byte));
-                if (c0 + 256 * i < a.cols) *reinterpret_cast<uint2 *>(codes + c0 + 256 * i) = q;
-                word |= byte << (8 * (2 * i + half));
-            }
+            Bf16x16 v = {};
+            if (ok) v = load_bf16x16(static_cast<const uint16_t *>(a.X) + u.row * a.ldx + c, a.v32);
+            byte = b8_scale_byte<TYPE>(eighth_max(bf16x16_absmax(v)) << 16);
+            q = b8_encode_bf16x16<TYPE>(v, b8_inv_scale(byte));
         } else {
-            float4 v[2][2];
-            const float *x = static_cast<const float *>(a.X) + u.row * a.ldx;
+            float4 v[4];
+            const float4 *x = reinterpret_cast<const float4 *>(static_cast<const float *>(a.X) + u.row * a.ldx + c);
+            uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    v[i][h] = c0 + 256 * i < a.cols ? __ldg(reinterpret_cast<const float4 *>(x + c0 + 256 * i) + h)
-                                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    m = max(m, max(max(__float_as_uint(v[i][h].x) & 0x7fffffffu, __float_as_uint(v[i][h].y) & 0x7fffffffu),
-                                   max(__float_as_uint(v[i][h].z) & 0x7fffffffu, __float_as_uint(v[i][h].w) & 0x7fffffffu)));
-                }
-                const uint32_t byte = b8_scale_byte<TYPE>(half_warp_max(m));
-                const float inv = b8_inv_scale(byte);
-                uint32_t q[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    q[h] = inv == 0.0f ? 0u : b8_scale_encode4<TYPE>(v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w, inv);
-                if (c0 + 256 * i < a.cols) *reinterpret_cast<uint2 *>(codes + c0 + 256 * i) = make_uint2(q[0], q[1]);
-                word |= byte << (8 * (2 * i + half));
+            for (int h = 0; h < 4; ++h) {
+                v[h] = ok ? __ldg(x + h) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                m = max(m, max(max(__float_as_uint(v[h].x) & 0x7fffffffu, __float_as_uint(v[h].y) & 0x7fffffffu),
+                               max(__float_as_uint(v[h].z) & 0x7fffffffu, __float_as_uint(v[h].w) & 0x7fffffffu)));
             }
+            byte = b8_scale_byte<TYPE>(eighth_max(m));
+            const float inv = b8_inv_scale(byte);
+            uint32_t p[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) p[h] = b8_scale_encode4<TYPE>(v[h].x, v[h].y, v[h].z, v[h].w, inv);
+            q = inv == 0.0f ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(p[0], p[1], p[2], p[3]);
         }
-        word |= __shfl_xor_sync(0xffffffffu, word, 16);
+        if (ok) *reinterpret_cast<uint4 *>(codes + c) = q;
+        const uint32_t word = scale_word(byte, lane);
         if (lane == 0) scales[w * a.rp] = word;
     }
 }
@@ -94,7 +80,7 @@ struct B8ReadArgs {
     int64_t ldc;
     const uint32_t *scales;
     int64_t rp;
-    int32_t rows, cols, words, per_warp;
+    int32_t rows, cols, words, per_warp, v32;
     uint16_t *X;
     int64_t ldx;
 };
@@ -103,22 +89,25 @@ template <int TYPE>
 __global__ void __launch_bounds__(256) b8_dequantize_kernel(B8ReadArgs a)
 {
     grid_wait_and_release();
-    const int lane = threadIdx.x & 31, half = lane >> 4;
+    const int lane = threadIdx.x & 31;
     const B8Walk u = b8_walk(a.words, a.per_warp);
     if (u.row >= a.rows) return;
     const uint32_t *scales = a.scales + b8_word_index(0, a.rp, u.row);
-    const int l0 = 128 * half + 8 * (lane & 15);
     for (int w = u.w0; w < u.w1; w += u.step) {
-        const int c0 = 512 * w + l0;
-        const uint32_t word = __ldg(scales + w * a.rp);
+        const int c = 512 * w + 16 * lane;
+        if (c >= a.cols) continue;
+        const float s = b8_scale((__ldg(scales + w * a.rp) >> (8 * (lane >> 3))) & 0xffu);
+        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(a.codes + u.row * a.ldc + c));
+        const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
+        Bf16x16 r;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (c0 + 256 * i >= a.cols) continue;
-            const uint2 q = __ldg(reinterpret_cast<const uint2 *>(a.codes + u.row * a.ldc + c0 + 256 * i));
-            float v[8];
-            b8_load8<TYPE>(q, b8_scale((word >> (8 * (2 * i + half))) & 0xffu), v);
-            *reinterpret_cast<uint4 *>(a.X + u.row * a.ldx + c0 + 256 * i) = pack_bf16x8(v);
+        for (int i = 0; i < 4; ++i) {
+            float v[4];
+            b8_decode4<TYPE>(qw[i], v);
+            r.w[2 * i] = pack_bf16(__fmul_rn(v[0], s), __fmul_rn(v[1], s));
+            r.w[2 * i + 1] = pack_bf16(__fmul_rn(v[2], s), __fmul_rn(v[3], s));
         }
+        store_bf16x16(a.X + u.row * a.ldx + c, r, a.v32);
     }
 }
 

@@ -133,6 +133,9 @@ static bool complete(const sbl_b8 *m) { return m && m->codes && m->scales; }
 static bool b8_aligned(const sbl_b8 *m) { return aligned16(m->codes) && aligned16(m->scales); }
 static uint32_t *scale_words(const sbl_b8 *m) { return reinterpret_cast<uint32_t *>(m->scales); }
 
+// Whether every row of a strided bf16 matrix is 32-byte aligned (nullptr: yes).
+static bool rows32(const void *p, int64_t ld) { return !p || ((reinterpret_cast<uintptr_t>(p) & 31u) == 0 && ld % 16 == 0); }
+
 // A strided bf16 (or fp32) matrix of `cols` columns: 16-byte aligned rows.
 static sbl_status check_strided(const void *p, int64_t ld, int64_t cols, int elem_bytes)
 {
@@ -155,6 +158,7 @@ static sbl_status quantize_rows(const HostDevice &hd, const sbl_b8_desc *d, cons
     a.scales = scale_words(out);
     a.rp = b8_rp(d->rows);
     a.words = b8_words(d->cols);
+    a.v32 = rows32(X, ldx);
     return launch_walk(hd, b8_quantize_rows_kernel<TYPE, SRC>, a.rp, a, stream);
 }
 
@@ -618,6 +622,7 @@ sbl_status sbl_b8_dequantize(const sbl_b8_desc *desc, const sbl_b8 *in, uint16_t
     a.words = b8_words(desc->cols);
     a.X = X;
     a.ldx = ldx;
+    a.v32 = rows32(X, ldx);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (desc->type) {
     case SBL_B8_E4M3: return launch_walk(hd, b8_dequantize_kernel<kB8E4M3>, a.rows, a, s);
@@ -760,6 +765,7 @@ sbl_status sbl_glu_forward(const sbl_b8_desc *desc, sbl_activation act, const ui
     a.rows = desc->rows;
     a.cols = desc->cols;
     a.words = b8_words(desc->cols);
+    a.v32 = rows32(G, ldg) && rows32(U, ldu) && rows32(H, ldh);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (desc->type * 2 + act) {
     case SBL_B8_E4M3 * 2 + SBL_ACT_SILU: return glu_forward<kB8E4M3, kActSilu>(hd, a, s);
@@ -801,6 +807,7 @@ sbl_status sbl_glu_backward(const sbl_b8_desc *desc, sbl_activation act, const s
     a.rows = desc->rows;
     a.cols = desc->cols;
     a.words = b8_words(desc->cols);
+    a.v32 = rows32(dH, lddh) && rows32(dG, lddg) && rows32(dU, lddu);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (desc->type * 2 + act) {
     case SBL_B8_E4M3 * 2 + SBL_ACT_SILU: return glu_backward<kB8E4M3, kActSilu>(hd, a, s);

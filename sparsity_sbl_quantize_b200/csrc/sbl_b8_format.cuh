@@ -53,16 +53,16 @@ __host__ __device__ __forceinline__ int64_t b8_word_index(int64_t w, int64_t rp,
 }
 
 // The scale byte for a block whose largest magnitude has the fp32 bits `a`.
+// With MAX = (1 + top / 2^23) 2^shift the exponent is a's own less shift, and one
+// more when a's fraction exceeds top: adding 2^23 - 1 - top carries exactly then.
 template <int TYPE>
 __device__ __forceinline__ uint32_t b8_scale_byte(uint32_t a)
 {
-    if (a >= kF32Inf) return 255u;
-    if (a == 0u) return 127u;
-    // MAX = (1 + top / 2^23) 2^shift
     constexpr int shift = TYPE == kB8E4M3 ? 8 : TYPE == kB8E5M2 ? 15 : 6;
-    constexpr uint32_t top = TYPE == kB8I8 ? 0x7e0000u : 0x600000u;
-    const int e = static_cast<int>(a >> 23) - shift + ((a & 0x7fffffu) > top ? 1 : 0);
-    return static_cast<uint32_t>(e < 1 ? 1 : e);
+    constexpr int top = TYPE == kB8I8 ? 0x7e0000 : 0x600000;
+    constexpr int add = 0x7fffff - top - (shift << 23);
+    const int e = max(static_cast<int>(a) + add, 1 << 23) >> 23;
+    return a >= kF32Inf ? 255u : a == 0u ? 127u : static_cast<uint32_t>(e);
 }
 
 // 2^-(byte - 127), exact; 0 for a block that is not finite (its codes are 0)
@@ -160,12 +160,82 @@ __device__ __forceinline__ B8Walk b8_walk(int words, int per_warp)
     return {static_cast<int64_t>(blockIdx.x) * 8 + v, w0, min(w0 + per_warp, words), 1};
 }
 
-// max over the 16 lanes of a half warp, of two 16-bit magnitudes at once
-__device__ __forceinline__ uint32_t half_warp_max2(uint32_t v)
+// Sixteen bf16 of a row, one lane's share in the element-wise kernels: 32-byte
+// accesses where every row is 32-byte aligned (v32), pairs of 16-byte ones
+// otherwise.
+struct Bf16x16 {
+    uint32_t w[8];
+};
+
+__device__ __forceinline__ Bf16x16 load_bf16x16(const uint16_t *p, bool v32)
+{
+    Bf16x16 r;
+    if (v32) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p)), b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+        r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+        r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
+    }
+    return r;
+}
+
+__device__ __forceinline__ void store_bf16x16(uint16_t *p, const Bf16x16 &r, bool v32)
+{
+    if (v32) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]),
+                     "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
+    }
+}
+
+// Largest |x| as bf16 bits, as bf16x8_absmax.
+__device__ __forceinline__ uint32_t bf16x16_absmax(const Bf16x16 &v)
+{
+    uint32_t m = v.w[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __vmaxu2(m, v.w[i] & 0x7fff7fffu);
+    return max(m & 0xffffu, m >> 16);
+}
+
+// Sixteen codes with the factor inv (0: a block that is not finite, codes 0).
+template <int TYPE>
+__device__ __forceinline__ uint4 b8_encode_bf16x16(const Bf16x16 &v, float inv)
+{
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        q[i] = b8_scale_encode4<TYPE>(bf16_lo(v.w[2 * i]), bf16_hi(v.w[2 * i]), bf16_lo(v.w[2 * i + 1]), bf16_hi(v.w[2 * i + 1]), inv);
+    return inv == 0.0f ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(q[0], q[1], q[2], q[3]);
+}
+
+// max over the 8 lanes that hold a block (sixteen values each)
+__device__ __forceinline__ uint32_t eighth_max(uint32_t v)
 {
 #pragma unroll
-    for (int off = 8; off > 0; off >>= 1) v = __vmaxu2(v, __shfl_xor_sync(0xffffffffu, v, off));
+    for (int off = 4; off > 0; off >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, off));
     return v;
+}
+
+// The same for two 16-bit magnitudes at once.
+__device__ __forceinline__ uint32_t eighth_max2(uint32_t v)
+{
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) v = __vmaxu2(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
+// The warp's scale word from its four blocks' bytes (lanes 8 b .. hold block b's).
+__device__ __forceinline__ uint32_t scale_word(uint32_t byte, int lane)
+{
+    uint32_t w = byte << (8 * (lane >> 3));
+    w |= __shfl_xor_sync(0xffffffffu, w, 8);
+    return w | __shfl_xor_sync(0xffffffffu, w, 16);
 }
 
 // max over the 16 lanes of a half warp

@@ -75,14 +75,14 @@ struct GluFwdArgs {
     uint32_t *gs, *us;
     int64_t ldc;
     int64_t rp;
-    int32_t rows, cols, words, per_warp;
+    int32_t rows, cols, words, per_warp, v32;
 };
 
 template <int TYPE, int ACT, bool GATED>
 __global__ void __launch_bounds__(256) glu_forward_kernel(GluFwdArgs a)
 {
     grid_wait_and_release();
-    const int lane = threadIdx.x & 31, half = lane >> 4;
+    const int lane = threadIdx.x & 31;
     const B8Walk wk = b8_walk(a.words, a.per_warp);
     if (wk.row >= a.rp) return;
     const int64_t wi = b8_word_index(0, a.rp, wk.row);
@@ -94,51 +94,38 @@ __global__ void __launch_bounds__(256) glu_forward_kernel(GluFwdArgs a)
             }
         return;
     }
-    const int l0 = 128 * half + 8 * (lane & 15);
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
     const uint16_t *G = a.G + wk.row * a.ldg, *U = GATED ? a.U + wk.row * a.ldu : nullptr;
     for (int w = wk.w0; w < wk.w1; w += wk.step) {
-        const int c0 = 512 * w + l0;
-        uint4 g[2], u[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const bool ok = c0 + 256 * i < a.cols;
-            g[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(G + c0 + 256 * i)) : z;
-            if (GATED) u[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(U + c0 + 256 * i)) : z;
+        const int c = 512 * w + 16 * lane;
+        const bool ok = c < a.cols;
+        Bf16x16 g = {}, u = {};
+        if (ok) {
+            g = load_bf16x16(G + c, a.v32);
+            if (GATED) u = load_bf16x16(U + c, a.v32);
         }
-        uint32_t gw = 0, uw = 0;
+        if (a.H && ok) {
+            Bf16x16 h;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int c = c0 + 256 * i;
-            const bool ok = c < a.cols;
-            if (a.H && ok) {
-                float gv[8], uv[8], h[8];
-                unpack_bf16x8(g[i], gv);
-                if (GATED) unpack_bf16x8(u[i], uv);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) h[k] = GATED ? act_value<ACT>(gv[k]) * uv[k] : act_value<ACT>(gv[k]);
-                *reinterpret_cast<uint4 *>(a.H + wk.row * a.ldh + c) = pack_bf16x8(h);
+            for (int i = 0; i < 8; ++i) {
+                float lo = act_value<ACT>(bf16_lo(g.w[i])), hi = act_value<ACT>(bf16_hi(g.w[i]));
+                if (GATED) lo *= bf16_lo(u.w[i]), hi *= bf16_hi(u.w[i]);
+                h.w[i] = pack_bf16(lo, hi);
             }
-            // the largest magnitudes of both blocks in one reduction
-            const uint32_t top = half_warp_max2(bf16x8_absmax(g[i]) | (GATED ? bf16x8_absmax(u[i]) << 16 : 0u));
-            if (a.gc) {
-                const uint32_t byte = b8_scale_byte<TYPE>(top << 16);
-                if (ok) *reinterpret_cast<uint2 *>(a.gc + wk.row * a.ldc + c) = b8_encode_bf16x8<TYPE>(g[i], b8_inv_scale(byte));
-                gw |= byte << (8 * (2 * i + half));
-            }
-            if (GATED && a.uc) {
-                const uint32_t byte = b8_scale_byte<TYPE>(top & 0xffff0000u);
-                if (ok) *reinterpret_cast<uint2 *>(a.uc + wk.row * a.ldc + c) = b8_encode_bf16x8<TYPE>(u[i], b8_inv_scale(byte));
-                uw |= byte << (8 * (2 * i + half));
-            }
+            store_bf16x16(a.H + wk.row * a.ldh + c, h, a.v32);
         }
+        // the largest magnitudes of both blocks in one reduction
+        const uint32_t top = eighth_max2(bf16x16_absmax(g) | (GATED ? bf16x16_absmax(u) << 16 : 0u));
         if (a.gc) {
-            gw |= __shfl_xor_sync(0xffffffffu, gw, 16);
-            if (lane == 0) a.gs[wi + w * a.rp] = gw;
+            const uint32_t byte = b8_scale_byte<TYPE>(top << 16);
+            if (ok) *reinterpret_cast<uint4 *>(a.gc + wk.row * a.ldc + c) = b8_encode_bf16x16<TYPE>(g, b8_inv_scale(byte));
+            const uint32_t word = scale_word(byte, lane);
+            if (lane == 0) a.gs[wi + w * a.rp] = word;
         }
         if (GATED && a.uc) {
-            uw |= __shfl_xor_sync(0xffffffffu, uw, 16);
-            if (lane == 0) a.us[wi + w * a.rp] = uw;
+            const uint32_t byte = b8_scale_byte<TYPE>(top & 0xffff0000u);
+            if (ok) *reinterpret_cast<uint4 *>(a.uc + wk.row * a.ldc + c) = b8_encode_bf16x16<TYPE>(u, b8_inv_scale(byte));
+            const uint32_t word = scale_word(byte, lane);
+            if (lane == 0) a.us[wi + w * a.rp] = word;
         }
     }
 }
@@ -152,50 +139,46 @@ struct GluBwdArgs {
     int64_t ldh;
     uint16_t *dG, *dU;
     int64_t ldg, ldu;
-    int32_t rows, cols, words, per_warp;
+    int32_t rows, cols, words, per_warp, v32;
 };
 
 template <int TYPE, int ACT, bool GATED>
 __global__ void __launch_bounds__(256) glu_backward_kernel(GluBwdArgs a)
 {
     grid_wait_and_release();
-    const int lane = threadIdx.x & 31, half = lane >> 4;
+    const int lane = threadIdx.x & 31;
     const B8Walk wk = b8_walk(a.words, a.per_warp);
     if (wk.row >= a.rows) return;
     const int64_t wi = b8_word_index(0, a.rp, wk.row);
-    const int l0 = 128 * half + 8 * (lane & 15);
     for (int w = wk.w0; w < wk.w1; w += wk.step) {
-        const int c0 = 512 * w + l0;
+        const int c = 512 * w + 16 * lane, sh = 8 * (lane >> 3);
+        if (c >= a.cols) continue;
         const uint32_t gw = __ldg(a.gs + wi + w * a.rp), uw = GATED ? __ldg(a.us + wi + w * a.rp) : 0u;
-        uint2 gq[2], uq[2];
-        uint4 hq[2];
+        const uint4 gq = __ldg(reinterpret_cast<const uint4 *>(a.gc + wk.row * a.ldc + c));
+        const uint4 uq = GATED ? __ldg(reinterpret_cast<const uint4 *>(a.uc + wk.row * a.ldc + c)) : make_uint4(0u, 0u, 0u, 0u);
+        const Bf16x16 dh = load_bf16x16(a.dH + wk.row * a.ldh + c, a.v32);
+        const float gsc = b8_scale((gw >> sh) & 0xffu), usc = GATED ? b8_scale((uw >> sh) & 0xffu) : 0.0f;
+        const uint32_t gqw[4] = {gq.x, gq.y, gq.z, gq.w}, uqw[4] = {uq.x, uq.y, uq.z, uq.w};
+        Bf16x16 dg, du;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int c = c0 + 256 * i;
-            if (c >= a.cols) continue;
-            gq[i] = __ldg(reinterpret_cast<const uint2 *>(a.gc + wk.row * a.ldc + c));
-            if (GATED) uq[i] = __ldg(reinterpret_cast<const uint2 *>(a.uc + wk.row * a.ldc + c));
-            hq[i] = __ldg(reinterpret_cast<const uint4 *>(a.dH + wk.row * a.ldh + c));
-        }
+        for (int i = 0; i < 4; ++i) {
+            float g[4], u[4], x[4], y[4];
+            b8_decode4<TYPE>(gqw[i], g);
+            if (GATED) b8_decode4<TYPE>(uqw[i], u);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int c = c0 + 256 * i;
-            if (c >= a.cols) continue;
-            const int sh = 8 * (2 * i + half);
-            float g[8], u[8], dh[8], dg[8], du[8];
-            b8_load8<TYPE>(gq[i], b8_scale((gw >> sh) & 0xffu), g);
-            if (GATED) b8_load8<TYPE>(uq[i], b8_scale((uw >> sh) & 0xffu), u);
-            unpack_bf16x8(hq[i], dh);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float v, d;
-                act_value_grad<ACT>(g[k], v, d);
-                dg[k] = GATED ? dh[k] * u[k] * d : dh[k] * d;
-                du[k] = dh[k] * v;
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t hw = dh.w[2 * i + (k >> 1)];
+                const float d = k & 1 ? bf16_hi(hw) : bf16_lo(hw);
+                float v, dv;
+                act_value_grad<ACT>(__fmul_rn(g[k], gsc), v, dv);
+                x[k] = GATED ? d * __fmul_rn(u[k], usc) * dv : d * dv;
+                y[k] = d * v;
             }
-            *reinterpret_cast<uint4 *>(a.dG + wk.row * a.ldg + c) = pack_bf16x8(dg);
-            if (GATED) *reinterpret_cast<uint4 *>(a.dU + wk.row * a.ldu + c) = pack_bf16x8(du);
+            dg.w[2 * i] = pack_bf16(x[0], x[1]), dg.w[2 * i + 1] = pack_bf16(x[2], x[3]);
+            if (GATED) du.w[2 * i] = pack_bf16(y[0], y[1]), du.w[2 * i + 1] = pack_bf16(y[2], y[3]);
         }
+        store_bf16x16(a.dG + wk.row * a.ldg + c, dg, a.v32);
+        if (GATED) store_bf16x16(a.dU + wk.row * a.ldu + c, du, a.v32);
     }
 }
 
