@@ -85,6 +85,28 @@ static sbl_status launch(void (*kernel)(P...), int64_t grid, int block, size_t s
     return launch2(kernel, grid, 1, block, smem, stream, args...);
 }
 
+// The same in clusters of `cluster` CTAs.
+template <typename... P, typename... A>
+static sbl_status launch_cluster(void (*kernel)(P...), int64_t grid, int cluster, int block, cudaStream_t stream, A... args)
+{
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(block));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return SBL_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? SBL_OK : SBL_ERR_CUDA;
+}
+
 // Scale words (512 columns) a warp of the element-wise kernels takes: one
 // while the rows alone do not fill the device twice over, four after that.
 static int32_t words_per_warp(int64_t rows, int32_t words, int num_sms)
@@ -506,41 +528,44 @@ static sbl_status norm_checkpoint(const uint16_t *X, int32_t T, int32_t K, const
     return SBL_ERR_SHAPE;
 }
 
-// Threads that share a row in the backward: two 8-element chunks each (rows
-// over 8192: see norm_backward).
+// Threads that share a row in the backward, one 16-element chunk each, and the
+// CTAs a longer row is split over.
 static int norm_row_threads(int32_t K)
 {
     int rt = 32;
-    while (rt < 1024 && rt * 2 < K / 8) rt *= 2;
+    while (rt < kNormLongThreads && rt < K / 16) rt *= 2;
     return rt;
 }
 
-// About 1024 threads an SM, each keeping its columns' part of the gains'
-// gradient while it goes through the rows.
-static int64_t norm_grid(int32_t T, int32_t K, int num_sms)
+static int norm_split(int32_t K)
+{
+    int split = 1;
+    while (split * kNormLongThreads < K / 16) split *= 2;
+    return split;
+}
+
+// Units (CTAs, or clusters for long rows) that go through the rows: the 512
+// threads that fit an SM at 126 registers.
+static int64_t norm_units(int32_t T, int32_t K, int num_sms)
 {
     const int rt = norm_row_threads(K);
     const int rows = rt >= 256 ? 1 : 256 / rt, block = std::max(rt, 256);
-    return std::min<int64_t>({(static_cast<int64_t>(T) + rows - 1) / rows, 1024ll / block * num_sms, kNormPartials});
+    return std::min<int64_t>({(static_cast<int64_t>(T) + rows - 1) / rows, static_cast<int64_t>(512 / block) * num_sms / norm_split(K),
+                              kNormPartials});
 }
 
 template <int TYPE>
-static sbl_status norm_backward(const NormBwdArgs &a, int64_t grid, cudaStream_t stream)
+static sbl_status norm_backward(NormBwdArgs a, int64_t units, cudaStream_t stream)
 {
-    // Longer rows do not leave registers for the next row's loads and spill: 16384 x 11008
-    // runs at 2.3 TB/s where 16384 x 2048 reaches 4.9.
+    a.split = norm_split(a.K);
     const int rt = norm_row_threads(a.K);
     const size_t smem = rt < 256 && a.partial ? static_cast<size_t>(a.K) * 4 : 0;
     switch (rt) {
-    case 32: return launch(norm_backward_kernel<TYPE, 32, 2, true>, grid, 256, smem, stream, a);
-    case 64: return launch(norm_backward_kernel<TYPE, 64, 2, true>, grid, 256, smem, stream, a);
-    case 128: return launch(norm_backward_kernel<TYPE, 128, 2, true>, grid, 256, smem, stream, a);
-    case 256: return launch(norm_backward_kernel<TYPE, 256, 2, true>, grid, 256, smem, stream, a);
-    case 512: return launch(norm_backward_kernel<TYPE, 512, 2, true>, grid, 512, smem, stream, a);
-    default:
-        return a.K <= 512 * 4 * 8    ? launch(norm_backward_kernel<TYPE, 512, 4, false>, grid, 512, smem, stream, a)
-               : a.K <= 1024 * 2 * 8 ? launch(norm_backward_kernel<TYPE, 1024, 2, false>, grid, 1024, smem, stream, a)
-                                     : launch(norm_backward_kernel<TYPE, 1024, 8, false>, grid, 1024, smem, stream, a);
+    case 32: return launch(norm_backward_kernel<TYPE, 32>, units, 256, smem, stream, a);
+    case 64: return launch(norm_backward_kernel<TYPE, 64>, units, 256, smem, stream, a);
+    case 128: return launch(norm_backward_kernel<TYPE, 128>, units, 256, smem, stream, a);
+    case 256: return launch(norm_backward_kernel<TYPE, 256>, units, 256, smem, stream, a);
+    default: return launch_cluster(norm_backward_kernel<TYPE, kNormLongThreads>, units * a.split, a.split, kNormLongThreads, stream, a);
     }
 }
 
@@ -883,15 +908,16 @@ sbl_status sbl_rmsnorm_backward(const sbl_b8_desc *desc, const sbl_b8 *x8, const
     a.partial = dg ? static_cast<float *>(workspace) : nullptr;
     a.T = T;
     a.K = K;
+    a.v32 = rows32(dU, K) && rows32(dR, K) && rows32(dX, K);
     a.eps = static_cast<float>(eps);
-    const int64_t grid = norm_grid(T, K, hd.num_sms);
+    const int64_t units = norm_units(T, K, hd.num_sms);
     switch (desc->type) {
-    case SBL_B8_E4M3: st = norm_backward<kB8E4M3>(a, grid, s); break;
-    case SBL_B8_E5M2: st = norm_backward<kB8E5M2>(a, grid, s); break;
-    default: st = norm_backward<kB8I8>(a, grid, s); break;
+    case SBL_B8_E4M3: st = norm_backward<kB8E4M3>(a, units, s); break;
+    case SBL_B8_E5M2: st = norm_backward<kB8E5M2>(a, units, s); break;
+    default: st = norm_backward<kB8I8>(a, units, s); break;
     }
     if (st != SBL_OK || !dg) return st;
-    return launch(norm_dgain_kernel, (K + 31) / 32, 1024, 0, s, static_cast<const float *>(a.partial), static_cast<int32_t>(grid), K, dg);
+    return launch(norm_dgain_kernel, (K + 31) / 32, 1024, 0, s, static_cast<const float *>(a.partial), static_cast<int32_t>(units), K, dg);
 }
 
 }  // extern "C"

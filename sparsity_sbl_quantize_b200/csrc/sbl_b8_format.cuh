@@ -182,6 +182,23 @@ __device__ __forceinline__ Bf16x16 load_bf16x16(const uint16_t *p, bool v32)
     return r;
 }
 
+// The same from memory that this kernel may also write.
+__device__ __forceinline__ Bf16x16 load_bf16x16_plain(const uint16_t *p, bool v32)
+{
+    Bf16x16 r;
+    if (v32) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
+                     : "l"(p)
+                     : "memory");
+    } else {
+        const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
+        r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+        r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
+    }
+    return r;
+}
+
 __device__ __forceinline__ void store_bf16x16(uint16_t *p, const Bf16x16 &r, bool v32)
 {
     if (v32) {

@@ -185,13 +185,19 @@ __global__ void __launch_bounds__(256) glu_backward_kernel(GluBwdArgs a)
 // RMSNorm backward from the checkpointed input.  With v_k = du_k gain_k,
 //   r = (sum x^2 / K + eps)^-1/2,  c = r^3 / K sum_k v_k x_k,
 //   dx_k = r v_k - c x_k (+ residual gradient),   dgain_k = sum_t du x r.
-// RT threads share a row; thread lt holds the 8-element chunks lt + j RT
-// (j < NC), so both sums are one pass over registers and the row is read
-// once.  A CTA takes rows in steps of the grid and keeps its part of dgain in
+// RT threads share a row, one 16-element chunk each, so both sums are one pass
+// over registers and the row is read once; a row longer than
+// kNormLongThreads chunks is shared by a cluster of CTAs, which exchange their
+// sums.  A CTA takes rows in steps of the grid and keeps its part of dgain in
 // registers; the parts meet in shared memory (rows of one CTA, in order) and
 // then in norm_dgain_kernel (CTAs, in order), so the result is the same every
 // time.
-constexpr int kNormPartials = 640;  // most CTAs that leave a partial dgain
+// 16384 x 2048 with the residual gradient: 44 us, 5.3 TB/s (one row's latency, its
+// barrier and 126 registers a thread bound it, not DRAM); rows over 8192, with a
+// cluster barrier a row, 2.9 TB/s.
+constexpr int kNormPartials = 640;  // most partial rows of dgain
+constexpr int kNormLongThreads = 512;
+constexpr int kNormMaxSplit = 8;    // CTAs a row: 8 x 512 chunks of 16 = 65536
 
 struct NormBwdArgs {
     const uint8_t *xc;
@@ -203,85 +209,82 @@ struct NormBwdArgs {
     uint16_t *dX;
     float *partial;        // [grid, K]; nullptr: no dgain
     int32_t T, K;
+    int32_t v32;           // every bf16 row is 32-byte aligned
+    int32_t split;         // CTAs that share a row (a cluster)
     float eps;
 };
 
-template <int TYPE, int RT, int NC, bool AHEAD>
+template <int TYPE, int RT>
 __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 2) norm_backward_kernel(NormBwdArgs a)
 {
     constexpr int kRows = RT >= 256 ? 1 : 256 / RT;  // rows of one step
     constexpr int W = RT / 32;
     __shared__ float2 red[2][kRows][W];
+    __shared__ float2 parts[2][kNormMaxSplit];  // a long row: the CTAs' sums
     extern __shared__ float dg_sh[];  // [K]
     grid_wait_and_release();
+    // every CTA of a cluster runs before one writes to another's shared memory
+    if (RT == kNormLongThreads && a.split > 1) cluster_sync_all();
     const int sub = threadIdx.x / RT, lt = threadIdx.x % RT;
-    const int chunks = a.K / 8;
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    const int chunks = a.K / 16;
+    const int rank = a.split > 1 ? static_cast<int>(blockIdx.x) % a.split : 0;
+    const int unit = static_cast<int>(blockIdx.x) / a.split, units = static_cast<int>(gridDim.x) / a.split;
+    const int ci = rank * RT + lt;  // this thread's chunk
+    const bool mine = ci < chunks;
     const float invk = 1.0f / static_cast<float>(a.K);
-    uint4 gain[NC];  // bf16 1.0 where there are none
-    const uint8_t *sbase[NC];  // scale byte of the chunk's block, without the row's part
+    Bf16x16 gain;  // bf16 1.0 where there are none
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-        const int ci = lt + j * RT, blk = ci >> 4;
-        gain[j] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-        if (a.gain && ci < chunks) gain[j] = __ldg(reinterpret_cast<const uint4 *>(a.gain) + ci);
-        sbase[j] = reinterpret_cast<const uint8_t *>(a.xs) + 4 * (blk >> 2) * a.rp + (blk & 3);
-    }
-    float acc[NC][8];
+    for (int k = 0; k < 8; ++k) gain.w[k] = 0x3f803f80u;
+    if (a.gain && mine) gain = load_bf16x16(a.gain + 16 * ci, false);
+    const int blk = ci >> 3;  // scale byte of the chunk's block, without the row's part
+    const uint8_t *sbase = reinterpret_cast<const uint8_t *>(a.xs) + 4 * (blk >> 2) * a.rp + (blk & 3);
+    float acc[16];
 #pragma unroll
-    for (int j = 0; j < NC; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[j][k] = 0.0f;
+    for (int k = 0; k < 16; ++k) acc[k] = 0.0f;
 
-    // a row as it is read; AHEAD: the next one's loads are in flight while this
-    // one is worked on (not with 1024 threads, whose 64 registers would spill)
-    uint2 xq[NC];
-    uint4 du[NC], dr[NC];
-    uint32_t sb[NC];
+    // a row as it is read: the next one's loads are in flight while this one
+    // is worked on
+    uint4 xq;
+    Bf16x16 du, dr;
+    uint32_t sb;
     auto load = [&](int64_t row) {
         const int64_t r127 = row & 127, rpart = 4 * (row - r127 + 4 * (r127 & 31) + (r127 >> 5));
-#pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            const int ci = lt + j * RT;
-            xq[j] = make_uint2(0u, 0u);
-            du[j] = dr[j] = z;
-            sb[j] = 127u;
-            if (row < a.T && ci < chunks) {
-                xq[j] = __ldg(reinterpret_cast<const uint2 *>(a.xc + row * a.ldc) + ci);
-                du[j] = __ldg(reinterpret_cast<const uint4 *>(a.dU + row * a.K) + ci);
-                if (a.dR) dr[j] = *(reinterpret_cast<const uint4 *>(a.dR + row * a.K) + ci);  // dR may be dX
-                sb[j] = __ldg(sbase[j] + rpart);
-            }
+        xq = make_uint4(0u, 0u, 0u, 0u);
+        du = dr = Bf16x16{};
+        sb = 127u;
+        if (row < a.T && mine) {
+            xq = __ldg(reinterpret_cast<const uint4 *>(a.xc + row * a.ldc) + ci);
+            du = load_bf16x16(a.dU + row * a.K + 16 * ci, a.v32);
+            if (a.dR) dr = load_bf16x16_plain(a.dR + row * a.K + 16 * ci, a.v32);  // dR may be dX
+            sb = __ldg(sbase + rpart);
         }
     };
     int parity = 0;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-    int64_t base = static_cast<int64_t>(blockIdx.x) * kRows;
-    if (AHEAD) load(base + sub);
+    const int64_t step = static_cast<int64_t>(units) * kRows;
+    int64_t base = static_cast<int64_t>(unit) * kRows;
+    load(base + sub);
     for (; base < a.T; base += step, parity ^= 1) {
         const int64_t row = base + sub;
         const bool active = row < a.T;
-        float x[NC][8];
-        uint4 cdu[NC], cdr[NC];
+        float x[16];
         float s1 = 0.0f, s2 = 0.0f;
-        if (!AHEAD) load(row);
+        const float sc = b8_scale(sb);
+        const uint32_t qw[4] = {xq.x, xq.y, xq.z, xq.w};
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            b8_load8<TYPE>(xq[j], b8_scale(sb[j]), x[j]);
-            cdu[j] = du[j];
-            cdr[j] = dr[j];
+        for (int i = 0; i < 4; ++i) {
+            float v[4];
+            b8_decode4<TYPE>(qw[i], v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[4 * i + k] = __fmul_rn(v[k], sc);
         }
-        if (AHEAD && base + step < a.T) load(row + step);
+        const Bf16x16 cdu = du, cdr = dr;
+        if (base + step < a.T) load(row + step);
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            float d[8], g[8];
-            unpack_bf16x8(cdu[j], d);
-            unpack_bf16x8(gain[j], g);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                s1 = fmaf(x[j][k], x[j][k], s1);
-                s2 = fmaf(d[k] * x[j][k], g[k], s2);
-            }
+        for (int k = 0; k < 8; ++k) {
+            const float x0 = x[2 * k], x1 = x[2 * k + 1];
+            s1 = fmaf(x1, x1, fmaf(x0, x0, s1));
+            s2 = fmaf(bf16_lo(cdu.w[k]) * x0, bf16_lo(gain.w[k]), s2);
+            s2 = fmaf(bf16_hi(cdu.w[k]) * x1, bf16_hi(gain.w[k]), s2);
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) {
@@ -301,47 +304,54 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 2) norm_ba
                 s2 += p.y;
             }
         }
-        const float r = rsqrtf(s1 * invk + a.eps);
-        const float c = r * r * r * (s2 * invk);
-        if (!active) continue;
-#pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            const int ci = lt + j * RT;
-            if (ci >= chunks) continue;
-            float d[8], g[8], e[8], o[8];
-            unpack_bf16x8(cdu[j], d);
-            unpack_bf16x8(gain[j], g);
-            unpack_bf16x8(cdr[j], e);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                acc[j][k] = fmaf(d[k] * x[j][k], r, acc[j][k]);
-                o[k] = fmaf(d[k], r * g[k], fmaf(-c, x[j][k], e[k]));
-            }
-            *(reinterpret_cast<uint4 *>(a.dX + row * a.K) + ci) = pack_bf16x8(o);
-        }
-    }
-    if (!a.partial) return;
-    for (int s = 0; s < kRows; ++s) {
-        if (sub == s) {
-#pragma unroll
-            for (int j = 0; j < NC; ++j) {
-                const int ci = lt + j * RT;
-                if (ci >= chunks) continue;
-                float *p = kRows > 1 ? dg_sh + 8 * ci : nullptr;
-                float *o = a.partial + static_cast<int64_t>(blockIdx.x) * a.K + 8 * ci;
-                if (kRows > 1 && s > 0)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) acc[j][k] += p[k];
-                if (s == kRows - 1) {
-                    reinterpret_cast<float4 *>(o)[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-                    reinterpret_cast<float4 *>(o)[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) p[k] = acc[j][k];
+        if constexpr (RT == kNormLongThreads) {
+            if (a.split > 1) {
+                // each CTA's sums to all of the cluster, then added in rank
+                // order; again two buffers and one barrier
+                if (lt < a.split)
+                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(map_shared_rank(smem_addr(&parts[parity][rank]), lt)),
+                                 "f"(s1), "f"(s2)
+                                 : "memory");
+                __syncwarp();
+                cluster_sync_all();
+                s1 = s2 = 0.0f;
+                for (int p = 0; p < a.split; ++p) {
+                    s1 += parts[parity][p].x;
+                    s2 += parts[parity][p].y;
                 }
             }
         }
-        __syncthreads();
+        const float r = rsqrtf(s1 * invk + a.eps);
+        const float c = r * r * r * (s2 * invk);
+        if (!active || !mine) continue;
+        Bf16x16 o;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float d0 = bf16_lo(cdu.w[k]), d1 = bf16_hi(cdu.w[k]), x0 = x[2 * k], x1 = x[2 * k + 1];
+            acc[2 * k] = fmaf(d0 * x0, r, acc[2 * k]);
+            acc[2 * k + 1] = fmaf(d1 * x1, r, acc[2 * k + 1]);
+            o.w[k] = pack_bf16(fmaf(d0, r * bf16_lo(gain.w[k]), fmaf(-c, x0, bf16_lo(cdr.w[k]))),
+                               fmaf(d1, r * bf16_hi(gain.w[k]), fmaf(-c, x1, bf16_hi(cdr.w[k]))));
+        }
+        store_bf16x16(a.dX + row * a.K + 16 * ci, o, a.v32);
+    }
+    if (!a.partial) return;
+    float *p = kRows > 1 ? dg_sh + 16 * ci : nullptr;
+    float4 *o = reinterpret_cast<float4 *>(a.partial + static_cast<int64_t>(unit) * a.K + 16 * ci);
+    for (int s = 0; s < kRows; ++s) {
+        if (sub == s && mine) {
+            if (kRows > 1 && s > 0)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) acc[k] += p[k];
+            if (s == kRows - 1) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) o[q] = make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) p[k] = acc[k];
+            }
+        }
+        if (kRows > 1) __syncthreads();
     }
 }
 
