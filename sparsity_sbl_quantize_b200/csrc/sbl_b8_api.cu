@@ -378,7 +378,7 @@ static sbl_status launch_skinny_nt(const HostDevice &hd, const SkinnyPlan &p, co
 // Y [T, O] = X W^T for few tokens.  X: bf16 (quantised in the kernel, xq an
 // output) or nullptr (xq an input).
 static sbl_status skinny(const HostDevice &hd, const SkinnyPlan &p, const sbl_b8_desc *wd, const sbl_b8 *W, const sbl_b8_desc *xd,
-                         const uint16_t *X, int64_t ldx, const sbl_b8 *xq, void *Y, int64_t ldy, bool fp32, bool accumulate, bool w_early, cudaStream_t stream)
+                         const uint16_t *X, int64_t ldx, const sbl_b8 *xq, void *Y, int64_t ldy, bool fp32, bool accumulate, cudaStream_t stream)
 {
     SkinnyArgs a;
     memset(&a, 0, sizeof(a));
@@ -405,7 +405,6 @@ static sbl_status skinny(const HostDevice &hd, const SkinnyPlan &p, const sbl_b8
     a.ldy = ldy;
     a.y_fp32 = fp32 ? 1 : 0;
     a.accumulate = accumulate ? 1 : 0;
-    a.w_early = w_early ? 1 : 0;
     a.err = hd.err;
     const bool e5 = xd->type == SBL_B8_E5M2;
     if (!X) {
@@ -429,10 +428,10 @@ static sbl_status skinny(const HostDevice &hd, const SkinnyPlan &p, const sbl_b8
     }
 }
 
-// D = A B^T; every argument checked.  w_early: the kernel enqueued before does
-// not write B; late: it writes neither operand nor touches D.
+// D = A B^T; every argument checked.  late: the kernel enqueued before writes
+// neither operand and does not touch D.
 static sbl_status gemm(const HostDevice &hd, const sbl_b8_desc *ad, const sbl_b8 *A, const sbl_b8_desc *bd, const sbl_b8 *B, void *D,
-                       int64_t ldd, bool fp32, bool accumulate, bool w_early, bool late, cudaStream_t stream)
+                       int64_t ldd, bool fp32, bool accumulate, bool late, cudaStream_t stream)
 {
     B8GemmArgs args;
     memset(&args, 0, sizeof(args));
@@ -451,7 +450,7 @@ static sbl_status gemm(const HostDevice &hd, const sbl_b8_desc *ad, const sbl_b8
         const SkinnyPlan p = skinny_plan(hd.num_sms, bd->rows, bd->cols, ad->rows, false);
         // not for fp32 sums that need LONG, nor for a K whose scales do not fit
         if ((!fp32 || p.max_blocks <= kB8SegBlocks) && p.smem <= kB8SmemAll && p.tmem_cols <= kTmemCols)
-            return skinny(hd, p, bd, B, ad, nullptr, 0, A, D, ldd, fp32, accumulate, w_early, stream);
+            return skinny(hd, p, bd, B, ad, nullptr, 0, A, D, ldd, fp32, accumulate, stream);
     }
     // 128 x 256 tiles or 128 x 128 ones, of which a product with few tiles has
     // twice as many: the time of a launch in units of 10 ns fits
@@ -671,7 +670,7 @@ sbl_status sbl_b8_gemm(const sbl_b8_desc *a_desc, const sbl_b8 *a, const sbl_b8_
     if (!b8_aligned(a) || !b8_aligned(b)) return SBL_ERR_ALIGNMENT;
     HostDevice hd;
     if ((st = b8_device(&hd)) != SBL_OK) return st;
-    return gemm(hd, a_desc, a, b_desc, b, D, ldd, d_is_fp32 != 0, accumulate != 0, false, false, static_cast<cudaStream_t>(stream));
+    return gemm(hd, a_desc, a, b_desc, b, D, ldd, d_is_fp32 != 0, accumulate != 0, false, static_cast<cudaStream_t>(stream));
 }
 
 // W [O, K] of a b8 linear: both sizes multiples of 16 up to 65536, a product type.
@@ -707,10 +706,10 @@ sbl_status sbl_b8_linear_forward(const sbl_b8_desc *w_desc, const sbl_b8 *w, con
     if (T <= 64) {
         const SkinnyPlan p = skinny_plan(hd.num_sms, w_desc->rows, w_desc->cols, T, true);
         if (p.smem <= kB8SmemAll && p.tmem_cols <= kTmemCols && static_cast<int64_t>(T) * p.max_blocks <= 112 && !(y_is_fp32 && p.max_blocks > kB8SegBlocks))
-            return skinny(hd, p, w_desc, w, &xd, X, ldx, xq, Y, ldy, y_is_fp32 != 0, false, false, s);
+            return skinny(hd, p, w_desc, w, &xd, X, ldx, xq, Y, ldy, y_is_fp32 != 0, false, s);
     }
     if ((st = quantize(hd, &xd, X, false, ldx, false, xq, nullptr, s)) != SBL_OK) return st;
-    return gemm(hd, &xd, xq, w_desc, w, Y, ldy, y_is_fp32 != 0, false, true, false, s);
+    return gemm(hd, &xd, xq, w_desc, w, Y, ldy, y_is_fp32 != 0, false, false, s);
 }
 
 size_t sbl_b8_linear_workspace_bytes(const sbl_b8_desc *w_desc, int32_t T)
@@ -755,9 +754,9 @@ sbl_status sbl_b8_linear_backward(const sbl_b8_desc *w_desc, const sbl_b8 *w_t, 
     if (dW && (st = transpose(&xd, xq, x_type, &xt, true, s)) != SBL_OK) return st;
     if (dX) {
         const sbl_b8_desc wt = {K, O, w_desc->type};
-        if ((st = gemm(hd, &p.g, &g, &wt, w_t, dX, K, dx_is_fp32 != 0, false, false, false, s)) != SBL_OK) return st;
+        if ((st = gemm(hd, &p.g, &g, &wt, w_t, dX, K, dx_is_fp32 != 0, false, false, s)) != SBL_OK) return st;
     }
-    if (dW) return gemm(hd, &p.gt, &gt, &p.xt, &xt, dW, K, true, dw_accumulate != 0, false, dX != nullptr, s);
+    if (dW) return gemm(hd, &p.gt, &gt, &p.xt, &xt, dW, K, true, dw_accumulate != 0, dX != nullptr, s);
     return SBL_OK;
 }
 

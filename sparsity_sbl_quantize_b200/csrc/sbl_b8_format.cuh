@@ -269,18 +269,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-__device__ __forceinline__ void unpack_bf16x8(const uint4 &q, float (&v)[8])
-{
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
-}
-
-__device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8])
-{
-    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-}
-
 // Eight codes of one block decoded with its scale s = 2^e.
 template <int TYPE>
 __device__ __forceinline__ void b8_load8(const uint2 &q, float s, float (&v)[8])

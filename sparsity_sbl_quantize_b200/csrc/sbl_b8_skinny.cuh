@@ -55,7 +55,6 @@ struct SkinnyArgs {
     int64_t ldy;
     int32_t y_fp32;
     int32_t accumulate;     // fp32 output: add to Y
-    int32_t w_early;        // W may be read before the previous kernel has ended
     uint32_t *err;
 };
 
@@ -119,27 +118,15 @@ __global__ void __launch_bounds__(kSkThreads)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const uint64_t pol = l2_evict_first_policy();
-    const int early = !FUSED && args.w_early ? min(args.stages, b1 - b0) : 0;
-    if (!FUSED && args.w_early && warp == 0 && lane == 0) {
-        // the kernel before this one quantises X and writes nothing of W:
-        // W is final (sbl_b8_device.cuh), and its loads need not wait for X
-        mbar_arrive_expect_tx(sf_bar, static_cast<uint32_t>(groups) * 1024u);
-        for (int g = 0; g < groups; ++g) bulk_load_1d(sfw_base + 512 * g, args.ws + (g0 + g) * args.wrp + row0, 512, sf_bar, pol);
-        for (int s = 0; s < early; ++s) {
-            mbar_arrive_expect_tx(full_bar(s), kStageBytes);
-            tma_load_2d(base + s * kStageBytes, &tmW, (b0 + s) * 128, row0, full_bar(s));
-        }
-    }
     grid_wait_and_release();
 
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         if (lane == 0) {
-            const bool w_early = !FUSED && args.w_early;
-            if (!w_early) mbar_arrive_expect_tx(sf_bar, static_cast<uint32_t>(groups) * (FUSED ? 512u : 1024u));
+            const uint64_t pol = l2_evict_first_policy();
+            mbar_arrive_expect_tx(sf_bar, static_cast<uint32_t>(groups) * (FUSED ? 512u : 1024u));
             for (int g = 0; g < groups; ++g) {
-                if (!w_early) bulk_load_1d(sfw_base + 512 * g, args.ws + (g0 + g) * args.wrp + row0, 512, sf_bar, pol);
+                bulk_load_1d(sfw_base + 512 * g, args.ws + (g0 + g) * args.wrp + row0, 512, sf_bar, pol);
                 if constexpr (!FUSED) bulk_load_1d(sfx_base + 512 * g, args.xs + (g0 + g) * args.xrp, 512, sf_bar, pol);
             }
         }
@@ -152,10 +139,8 @@ __global__ void __launch_bounds__(kSkThreads)
             if (!ok) break;
             if (lane == 0) {
                 const uint32_t s = base + stage * kStageBytes;
-                if (b - b0 >= early) {
-                    mbar_arrive_expect_tx(full_bar(stage), kStageBytes);
-                    tma_load_2d(s, &tmW, b * 128, row0, full_bar(stage));
-                }
+                mbar_arrive_expect_tx(full_bar(stage), kStageBytes);
+                tma_load_2d(s, &tmW, b * 128, row0, full_bar(stage));
                 if constexpr (!FUSED) tma_load_2d(s + kABytes, &tmX, b * 128, 0, full_bar(stage));
             }
             __syncwarp();
