@@ -554,3 +554,152 @@ def test_nothing_is_written_past_the_outputs(t, k, o):
     torch.cuda.synchronize()
     assert all(h.intact() for h in held)
     assert sbl.sbl_device_error() == 0
+
+
+@pytest.mark.parametrize("t", [1, 20, 64, 100, 300])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_linear_forward_into_a_wider_buffer(t, fp32):
+    sbl = sbl_mod()
+    o, k = 272, 1040
+    r = rng(t, 24)
+    w = r.standard_normal((o, k)).astype(np.float32)
+    x, xv = bf16(r.standard_normal((t, k)))
+    wd, wq = new(sbl, o, k, 0)
+    _, xq = new(sbl, t, k, 0)
+    sbl.sbl_b8_quantize(wd, torch.from_numpy(w).cuda(), wq, None, sbl.SBL_B8_TILES)
+    out = torch.full((t, o + 16), 3.0, dtype=torch.float32 if fp32 else torch.bfloat16, device="cuda")
+    sbl.sbl_b8_linear_forward(wd, wq, x, t, xq, out[:, :o])
+    check_product(out[:, :o].double().cpu().numpy(), ref.value(xv, 0), ref.value(w.astype(np.float64), 0, True),
+                  ref.HALF["fp32" if fp32 else "bf16"])
+    assert bool((out[:, o:] == 3.0).all())
+    check_stored(xq, k, 0, *ref.quantize(xv, 0))
+
+
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("outputs", ["h", "g", "u", "hg", "gu", "hu"])
+def test_glu_any_outputs(gated, outputs):
+    sbl = sbl_mod()
+    if not gated and "u" in outputs:
+        return  # refused: no checkpoint of an absent input
+    t, f = 37, 272
+    r = rng(25)
+    (g, gv), (u, uv) = bf16(r.standard_normal((t, f))), bf16(r.standard_normal((t, f)))
+    d, g8 = new(sbl, t, f, 0)
+    _, u8 = new(sbl, t, f, 0)
+    h = torch.full((t, f), 7.0, dtype=torch.bfloat16, device="cuda")
+    sbl.sbl_glu_forward(d, 1, g, u if gated else None, h if "h" in outputs else None, g8 if "g" in outputs else None,
+                        u8 if "u" in outputs else None)
+    want = ref.act(gv, 1)[0] * (uv if gated else 1.0)
+    if "h" in outputs:
+        assert (np.abs(h.double().cpu().numpy() - want) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + 2.0 ** -126).all()
+    else:
+        assert bool((h == 7.0).all())
+    for m, v, name in ((g8, gv, "g"), (u8, uv, "u")):
+        if name in outputs:
+            check_stored(m, f, 0, *ref.quantize(v, 0))
+        else:
+            assert bool((m.codes == 0xA5).all()) and bool((m.scales == 0xA5).all())
+
+
+@pytest.mark.parametrize("offset", [8, 16, 24])
+def test_rows_aligned_to_16_bytes_only(offset):
+    """Inputs and outputs that start `offset` elements into a buffer (16 bytes each step of 8)."""
+    sbl = sbl_mod()
+    t, f = 21, 528
+    r = rng(offset, 26)
+
+    def shifted(a=None):
+        buf = torch.zeros(t * f + 64, dtype=torch.bfloat16, device="cuda")
+        v = buf[offset:offset + t * f].view(t, f)
+        if a is not None:
+            v.copy_(a)
+        return v
+
+    (g, gv), (u, uv), (dh, dhv) = (bf16(r.standard_normal((t, f))) for _ in range(3))
+    d, g8 = new(sbl, t, f, 2)
+    _, u8 = new(sbl, t, f, 2)
+    h, dg, du, back = shifted(), shifted(), shifted(), shifted()
+    sbl.sbl_glu_forward(d, 1, shifted(g), shifted(u), h, g8, u8)
+    sbl.sbl_glu_backward(d, 1, g8, u8, shifted(dh), dg, du)
+    sbl.sbl_b8_dequantize(d, g8, back)
+    h2, dg2, du2, back2 = (torch.empty_like(g) for _ in range(4))
+    sbl.sbl_glu_forward(d, 1, g, u, h2, g8, u8)
+    sbl.sbl_glu_backward(d, 1, g8, u8, dh, dg2, du2)
+    sbl.sbl_b8_dequantize(d, g8, back2)
+    for a, b in ((h, h2), (dg, dg2), (du, du2), (back, back2)):
+        assert torch.equal(a, b)
+    x8, x8s = new(sbl, t, f, 0)[1], new(sbl, t, f, 0)[1]
+    d0 = sbl.b8_desc(t, f)
+    sbl.sbl_b8_quantize(d0, g, x8)
+    sbl.sbl_b8_quantize(d0, shifted(g), x8s)
+    assert torch.equal(x8.codes, x8s.codes) and torch.equal(x8.scales, x8s.scales)
+    dx, dxs = torch.empty_like(g), shifted()
+    sbl.sbl_rmsnorm_backward(d0, x8, None, 1e-5, u, dh, dx, None, None)
+    sbl.sbl_rmsnorm_backward(d0, x8, None, 1e-5, shifted(u), shifted(dh), dxs, None, None)
+    assert torch.equal(dx, dxs)
+
+
+def test_offsets_past_32_bits():
+    """Matrices of more than 2^32 elements: their last rows."""
+    sbl = sbl_mod()
+    rows, cols, n = 65700, 65536, 150
+    assert rows * cols > 1 << 32
+    tail, tv = bf16(rng(27).standard_normal((n, cols)))
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x[-n:] = tail
+    d = sbl.b8_desc(rows, cols)
+    q = sbl.alloc_b8(d)
+    sbl.sbl_b8_quantize(d, x, q)
+    y, e = ref.quantize(tv, 0)
+    assert np.array_equal(ref.code_values(0)[q.codes[-n:].cpu().numpy()], y)
+    out = torch.zeros_like(x)
+    sbl.sbl_b8_dequantize(d, q, out)
+    want = torch.from_numpy(ref.decode(y, e).astype(np.float32)).to(torch.bfloat16)
+    assert torch.equal(out[-n:].cpu(), want)
+    assert not out[:-n].any()
+    bd, b, bv = operands(sbl, rng(28), 16, cols, 0)
+    prod = torch.empty((rows, 16), dtype=torch.float32, device="cuda")
+    sbl.sbl_b8_gemm(d, q, bd, b, prod)
+    check_product(prod[-n:].double().cpu().numpy(), ref.decode(y, e), bv, ref.HALF["fp32"])
+    assert not prod[:-n].any()
+    dg = torch.zeros_like(x)
+    sbl.sbl_glu_backward(d, 1, q, None, x, dg, None)
+    g = ref.decode(y, e)
+    want = tv * 2 * np.maximum(g, 0)
+    assert (np.abs(dg[-n:].double().cpu().numpy() - want) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + 2.0 ** -126).all()
+    del out, dg, prod
+    qt = sbl.alloc_b8(sbl.b8_desc(cols, rows))
+    sbl.sbl_b8_transpose(d, q, qt)
+    # the last rows of the source are the last columns of the transpose; its blocks of 128 start at multiples of 128
+    first = (rows - n) // 128 * 128
+    lead = rows - n - first
+    blk = np.concatenate([np.zeros((lead, 64)), g[:, -64:]])
+    yt, _ = ref.quantize(np.ascontiguousarray(blk.T), 0)
+    assert np.array_equal(ref.code_values(0)[qt.codes[-64:, first:rows].cpu().numpy()], yt)
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    import subprocess
+    import sys
+    code = """
+import torch
+from sparsity_sbl_quantize_b200 import sbl
+wd = sbl.b8_desc(256, 512)
+w, x8 = sbl.alloc_b8(wd), sbl.alloc_b8(sbl.b8_desc(80, 512))
+W, X = torch.randn(256, 512, device="cuda"), torch.randn(80, 512, device="cuda").bfloat16()
+Y = torch.zeros(80, 256, device="cuda", dtype=torch.bfloat16)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    sbl.sbl_b8_quantize(wd, W, w, None, sbl.SBL_B8_TILES)
+    sbl.sbl_b8_linear_forward(wd, w, X, 80, x8, Y)
+g.replay()
+torch.cuda.synchronize()
+got = Y.clone()
+sbl.sbl_b8_linear_forward(wd, w, X, 80, x8, Y)
+torch.cuda.synchronize()
+assert torch.equal(got, Y) and bool(got.any()) and sbl.sbl_device_error() == 0
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stderr

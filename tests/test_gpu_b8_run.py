@@ -254,3 +254,41 @@ def test_timing_command(op):
     assert r.returncode == 0, r.stderr
     line = json.loads(r.stdout)
     assert line["op"] == op and line["iters"] == 2 and line["ms_per_call"] > 0
+
+
+@pytest.mark.parametrize("t,k,o", [(40, 512, 1040), (200, 1040, 272), (777, 1536, 1536), (2500, 2048, 1536)])
+def test_backward_calls_back_to_back(t, k, o):
+    """Calls that share weights and workspace, nothing waiting between them: each gets what it gets alone (the kernels of
+    one call start beside one another, and those of the next behind them)."""
+    sbl = sbl_mod()
+    gen = torch.Generator(device="cuda").manual_seed(t)
+    wd = sbl.b8_desc(o, k)
+    w, wt = sbl.alloc_b8(wd), sbl.alloc_b8(sbl.b8_desc(k, o))
+    sbl.sbl_b8_quantize(wd, torch.randn(o, k, generator=gen, device="cuda"), w, wt, sbl.SBL_B8_TILES)
+    ws = sbl.alloc_workspace(sbl.sbl_b8_linear_workspace_bytes(wd, t))
+    xs = [torch.randn(t, k, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(3)]
+    dys = [torch.randn(t, o, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(3)]
+    xq, y = sbl.alloc_b8(sbl.b8_desc(t, k)), torch.empty(t, o, dtype=torch.bfloat16, device="cuda")
+
+    def call(i, dx, dw):
+        sbl.sbl_b8_linear_forward(wd, w, xs[i], t, xq, y)
+        sbl.sbl_b8_linear_backward(wd, wt, xq, dys[i], t, dx, dw, ws)
+
+    def buffers():
+        return torch.full((t, k), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((o, k), 7.0, device="cuda")
+
+    want = []
+    for i in range(3):
+        b = buffers()
+        torch.cuda.synchronize()
+        call(i, *b)
+        torch.cuda.synchronize()
+        want.append(b)
+    got = [buffers() for _ in range(24)]
+    torch.cuda.synchronize()
+    for j, b in enumerate(got):
+        call(j % 3, *b)
+    torch.cuda.synchronize()
+    for j, b in enumerate(got):
+        assert torch.equal(b[0], want[j % 3][0]) and torch.equal(b[1], want[j % 3][1]), j
+    assert sbl.sbl_device_error() == 0
