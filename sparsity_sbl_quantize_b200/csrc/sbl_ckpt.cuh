@@ -322,7 +322,8 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 2) norm_ba
             }
         }
         const float r = rsqrtf(s1 * invk + a.eps);
-        const float c = r * r * r * (s2 * invk);
+        // in this order c stays in range where r^3 alone does not (r beyond 2^42 or below 2^-42)
+        const float c = r * (s2 * invk) * r * r;
         if (!active || !mine) continue;
         Bf16x16 o;
 #pragma unroll

@@ -703,3 +703,43 @@ print("ok")
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "ok" in r.stdout, r.stderr
+
+
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("t,k", [(5, 144), (3, 2064), (2, 8208)])
+@pytest.mark.parametrize("power", [-58, -45, 45, 56])
+def test_rmsnorm_backward_of_small_and_large_rows(typ, t, k, power):
+    """Rows whose r^3 is outside fp32's range while the gradient is not; eps 0.  The bounds are test_rmsnorm's."""
+    sbl = sbl_mod()
+    r = rng(typ, t, k, power + 100, 31)
+    (x, xv), (du, duv) = bf16(r.standard_normal((t, k)) * 2.0 ** power), bf16(r.standard_normal((t, k)))
+    g, gv = bf16(1 + 0.2 * r.standard_normal((1, k)))
+    d, x8 = new(sbl, t, k, typ)
+    sbl.sbl_b8_quantize(d, x, x8)
+    dx, dg = torch.empty_like(x), torch.empty(k, dtype=torch.float32, device="cuda")
+    ws = sbl.alloc_workspace(sbl.sbl_rmsnorm_backward_workspace_bytes(t, k))
+    sbl.sbl_rmsnorm_backward(d, x8, g.view(-1), 0.0, du, None, dx, dg, ws)
+    xq = ref.value(xv, typ)
+    wx, wg = ref.rmsnorm_backward(xq, gv, 0.0, duv)
+    rr = 1 / np.sqrt((xq * xq).mean(1, keepdims=True))
+    slack = 2.0 ** -24 * (90 * np.abs(xq) * rr ** 3 * (np.abs(duv * gv) * np.abs(xq)).mean(1, keepdims=True) +
+                          90 * np.abs(rr * duv * gv) + 2 * np.abs(wx))
+    assert (np.abs(dx.double().cpu().numpy() - wx) <= 2.0 ** -8 * np.abs(wx) + 2 * slack).all()
+    assert (np.abs(dg.double().cpu().numpy() - wg) <= 2.0 ** -24 * (t + 90) * np.abs(duv * xq * rr).sum(0)).all()
+
+
+def test_rmsnorm_backward_of_an_empty_row_with_a_small_eps():
+    """x = 0: dX = dU g / sqrt(eps), with r^3 = 1e45 out of range."""
+    sbl = sbl_mod()
+    r = rng(32)
+    du, duv = bf16(r.standard_normal((3, 272)))
+    x = torch.zeros_like(du)
+    x[1] = 1.0
+    d, x8 = new(sbl, 3, 272, 0)
+    sbl.sbl_b8_quantize(d, x, x8)
+    dx = torch.empty_like(x)
+    sbl.sbl_rmsnorm_backward(d, x8, None, 1e-30, du, None, dx, None, None)
+    want = duv[[0, 2]] * 1e15
+    got = dx.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    assert (np.abs(got[[0, 2]] - want) <= (2.0 ** -8 + 2.0 ** -20) * np.abs(want)).all()
