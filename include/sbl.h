@@ -624,7 +624,8 @@ sbl_status sbl_glu_forward(const sbl_b8_desc *desc, sbl_activation act, const ui
 
 /* Its gradient at the checkpointed values g, u:
  *   dG = dH * u * act'(g),  dU = dH * act(g)   (u8 and dU NULL: dG = dH act'(g)).
- * bf16 with row strides as above; u8 and dU go together. */
+ * bf16 with row strides as above; u8 and dU go together; no output may overlap
+ * an input. */
 sbl_status sbl_glu_backward(const sbl_b8_desc *desc, sbl_activation act, const sbl_b8 *g8, const sbl_b8 *u8, const uint16_t *dH,
                             int64_t lddh, uint16_t *dG, int64_t lddg, uint16_t *dU, int64_t lddu, void *stream);
 
@@ -643,7 +644,8 @@ sbl_status sbl_quantize_act_rmsnorm_checkpoint(const sbl_b8_desc *desc, const ui
  *              reaches x past the norm; NULL: none; may be the buffer dX),
  *   dg[k]    = sum_t dU x r   (NULL: not wanted; needs g).
  * dU, dR, dX: bf16 [T, K] contiguous; dg: fp32 [K], the same bits for the
- * same inputs on the same kind of device.  The quantiser's gradient is the
+ * same inputs on the same kind of device.  fp32 arithmetic: sum x^2 has to lie in
+ * its range (|x| up to about 2^56).  The quantiser's gradient is the
  * straight-through one of the summary pages (dU = the linear's dX).
  * workspace (dg only): sbl_rmsnorm_backward_workspace_bytes, 256-byte
  * aligned.  T == 0: dg zero.  One launch, two with dg. */

@@ -340,7 +340,7 @@ static SkinnyPlan skinny_plan(int num_sms, int32_t O, int32_t K, int32_t T, bool
     // an SM at least: at one to an SM the clusters of eight do not all find
     // room at once (2048 x 11008: 15.1 us instead of 7.9).
     const int64_t ctas = std::min<int64_t>(std::max<int64_t>((tiles * p.split + num_sms - 1) / num_sms, 2), 4);
-    const int64_t fixed = 1024 + (fused ? static_cast<int64_t>(p.max_blocks) * p.nt * kBKBytes : 0) + 1024 * p.max_groups + 512;
+    const int64_t fixed = 1024 + (fused ? static_cast<int64_t>(p.max_blocks) * p.nt * kBKBytes : 0) + 1024ll * p.max_groups + 512;
     const int64_t room = (kB8SmemAll - 1024 * ctas) / ctas - fixed;
     p.stages = static_cast<int>(std::max<int64_t>(2, std::min<int64_t>({p.max_blocks, room / skinny_stage_bytes(p.nt, fused), kSkMaxStages})));
     p.tmem_cols = 32;
