@@ -2,6 +2,7 @@
 // include/sbl.h: argument validation, tensor maps and launches.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -544,7 +545,7 @@ static int norm_split(int32_t K)
 }
 
 // Units (CTAs, or clusters for long rows) that go through the rows: the 512
-// threads that fit an SM at 126 registers.
+// threads that fit an SM at 128 registers.
 static int64_t norm_units(int32_t T, int32_t K, int num_sms)
 {
     const int rt = norm_row_threads(K);
@@ -908,7 +909,12 @@ sbl_status sbl_rmsnorm_backward(const sbl_b8_desc *desc, const sbl_b8 *x8, const
     a.T = T;
     a.K = K;
     a.v32 = rows32(dU, K) && rows32(dR, K) && rows32(dX, K);
-    a.eps = static_cast<float>(eps);
+    // eps = q 2^(2 (e - 127)), 1/4 <= q < 1
+    int exp2 = -2 * 1024;
+    const double frac = eps > 0.0 ? frexp(eps, &exp2) : 0.0;
+    const int half = (exp2 + 2049) / 2 - 1024;  // ceil(exp2 / 2)
+    a.eps_q = static_cast<float>(ldexp(frac, exp2 - 2 * half));
+    a.eps_e = half + 127;
     const int64_t units = norm_units(T, K, hd.num_sms);
     switch (desc->type) {
     case SBL_B8_E4M3: st = norm_backward<kB8E4M3>(a, units, s); break;

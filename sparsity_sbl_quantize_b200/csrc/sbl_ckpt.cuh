@@ -183,8 +183,14 @@ __global__ void __launch_bounds__(256) glu_backward_kernel(GluBwdArgs a)
 }
 
 // RMSNorm backward from the checkpointed input.  With v_k = du_k gain_k,
-//   r = (sum x^2 / K + eps)^-1/2,  c = r^3 / K sum_k v_k x_k,
-//   dx_k = r v_k - c x_k (+ residual gradient),   dgain_k = sum_t du x r.
+//   r = (sum x^2 / K + eps)^-1/2,  n_k = x_k r,  m = sum_k v_k n_k / K,
+//   dx_k = r (v_k - n_k m) (+ residual gradient),   dgain_k = sum_t du n.
+// Neither r^2, r^3 nor x^2 appears on its own: they leave fp32's range long
+// before x, r and dx do.  The row's sums are formed from the codes (x = code 2^e)
+// next to the largest exponent of the row that has a code other than zero, E:
+// sum x^2 = 2^2E s1 and sum v x = 2^E s2 with s1, s2 in range, and what a block
+// far below E loses is below the sums' last place.  eps joins them as
+// q 2^2Ee, 1/4 <= q < 1, at the larger of E and Ee.
 // RT threads share a row, one 16-element chunk each, so both sums are one pass
 // over registers and the row is read once; a row longer than
 // kNormLongThreads chunks is shared by a cluster of CTAs, which exchange their
@@ -193,7 +199,7 @@ __global__ void __launch_bounds__(256) glu_backward_kernel(GluBwdArgs a)
 // then in norm_dgain_kernel (CTAs, in order), so the result is the same every
 // time.
 // 16384 x 2048 with the residual gradient: 44 us, 5.3 TB/s (one row's latency, its
-// barrier and 126 registers a thread bound it, not DRAM); rows over 8192, with a
+// barrier and 128 registers a thread bound it, not DRAM); rows over 8192, with a
 // cluster barrier a row, 2.9 TB/s.
 constexpr int kNormPartials = 640;  // most partial rows of dgain
 constexpr int kNormLongThreads = 512;
@@ -211,16 +217,43 @@ struct NormBwdArgs {
     int32_t T, K;
     int32_t v32;           // every bf16 row is 32-byte aligned
     int32_t split;         // CTAs that share a row (a cluster)
-    float eps;
+    float eps_q;           // eps = eps_q 2^(2 (eps_e - 127))
+    int32_t eps_e;
 };
+
+// A row's sums so far: sum x^2 = s1 2^(2 (top - 127)), sum v x = s2 2^(top - 127);
+// top is a scale byte (0 for nothing but zeros, 255 for a block that is not finite).
+struct NormSums {
+    float s1, s2;
+    int top;
+};
+
+// 2^d, 0 below fp32's normal range (d <= 127)
+__device__ __forceinline__ float norm_pow2(int d) { return __uint_as_float(static_cast<uint32_t>(max(d + 127, 0)) << 23); }
+
+// `n` (a power of two up to 32) partial sums joined at the largest of their
+// exponents: lane l takes part l % n, and a butterfly adds them in one order.
+__device__ __forceinline__ NormSums norm_join(const NormSums *p, int n)
+{
+    NormSums s = p[threadIdx.x & (n - 1)];
+    const int top = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<uint32_t>(s.top)));
+    const float f = norm_pow2(s.top - top);
+    s = {s.s1 * f * f, s.s2 * f, top};
+#pragma unroll
+    for (int off = 1; off < n; off <<= 1) {
+        s.s1 += __shfl_xor_sync(0xffffffffu, s.s1, off);
+        s.s2 += __shfl_xor_sync(0xffffffffu, s.s2, off);
+    }
+    return s;
+}
 
 template <int TYPE, int RT>
 __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 2) norm_backward_kernel(NormBwdArgs a)
 {
     constexpr int kRows = RT >= 256 ? 1 : 256 / RT;  // rows of one step
     constexpr int W = RT / 32;
-    __shared__ float2 red[2][kRows][W];
-    __shared__ float2 parts[2][kNormMaxSplit];  // a long row: the CTAs' sums
+    __shared__ NormSums red[2][kRows][W];
+    __shared__ NormSums parts[2][kNormMaxSplit];  // a long row: the CTAs' sums
     extern __shared__ float dg_sh[];  // [K]
     grid_wait_and_release();
     // every CTA of a cluster runs before one writes to another's shared memory
@@ -266,73 +299,83 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 2) norm_ba
     for (; base < a.T; base += step, parity ^= 1) {
         const int64_t row = base + sub;
         const bool active = row < a.T;
-        float x[16];
-        float s1 = 0.0f, s2 = 0.0f;
-        const float sc = b8_scale(sb);
-        const uint32_t qw[4] = {xq.x, xq.y, xq.z, xq.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float v[4];
-            b8_decode4<TYPE>(qw[i], v);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[4 * i + k] = __fmul_rn(v[k], sc);
-        }
+        uint32_t qw[4] = {xq.x, xq.y, xq.z, xq.w};
+        // a block of zeros has no exponent (its byte stands for 2^0), one that
+        // is not finite the largest
+        constexpr uint32_t kMagnitude = TYPE == kB8I8 ? 0xffffffffu : 0x7f7f7f7fu;
+        const bool zeros = ((qw[0] | qw[1] | qw[2] | qw[3]) & kMagnitude) == 0u && sb != 255u;
+        const int byte = zeros ? 0 : static_cast<int>(sb);
         const Bf16x16 cdu = du, cdr = dr;
         if (base + step < a.T) load(row + step);
+        NormSums s = {byte == 255 ? __uint_as_float(0x7fc00000u) : 0.0f, 0.0f, 0};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float x0 = x[2 * k], x1 = x[2 * k + 1];
-            s1 = fmaf(x1, x1, fmaf(x0, x0, s1));
-            s2 = fmaf(bf16_lo(cdu.w[k]) * x0, bf16_lo(gain.w[k]), s2);
-            s2 = fmaf(bf16_hi(cdu.w[k]) * x1, bf16_hi(gain.w[k]), s2);
+        for (int i = 0; i < 4; ++i) {
+            float y[4];
+            b8_decode4<TYPE>(qw[i], y);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t dw = cdu.w[2 * i + (k >> 1)], gw = gain.w[2 * i + (k >> 1)];
+                s.s1 = fmaf(y[k], y[k], s.s1);
+                s.s2 = fmaf((k & 1 ? bf16_hi(dw) : bf16_lo(dw)) * (k & 1 ? bf16_hi(gw) : bf16_lo(gw)), y[k], s.s2);
+            }
         }
+        s.top = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<uint32_t>(byte)));
+        const float f = norm_pow2(byte - s.top);
+        s.s1 *= f * f;
+        s.s2 *= f;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) {
-            s1 += __shfl_xor_sync(0xffffffffu, s1, off);
-            s2 += __shfl_xor_sync(0xffffffffu, s2, off);
+            s.s1 += __shfl_xor_sync(0xffffffffu, s.s1, off);
+            s.s2 += __shfl_xor_sync(0xffffffffu, s.s2, off);
         }
         if constexpr (W > 1) {
             // two buffers in turn: one barrier (of the row's threads) a step
             // suffices
-            if ((lt & 31) == 0) red[parity][sub][lt >> 5] = make_float2(s1, s2);
+            if ((lt & 31) == 0) red[parity][sub][lt >> 5] = s;
             asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "n"(RT) : "memory");
-            s1 = s2 = 0.0f;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float2 p = red[parity][sub][w];
-                s1 += p.x;
-                s2 += p.y;
-            }
+            s = norm_join(red[parity][sub], W);
         }
         if constexpr (RT == kNormLongThreads) {
             if (a.split > 1) {
                 // each CTA's sums to all of the cluster, then added in rank
                 // order; again two buffers and one barrier
-                if (lt < a.split)
-                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(map_shared_rank(smem_addr(&parts[parity][rank]), lt)),
-                                 "f"(s1), "f"(s2)
-                                 : "memory");
+                if (lt < a.split) {
+                    const uint32_t to = map_shared_rank(smem_addr(&parts[parity][rank]), lt);
+                    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to), "f"(s.s1) : "memory");
+                    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to + 4u), "f"(s.s2) : "memory");
+                    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to + 8u), "r"(s.top) : "memory");
+                }
                 __syncwarp();
                 cluster_sync_all();
-                s1 = s2 = 0.0f;
-                for (int p = 0; p < a.split; ++p) {
-                    s1 += parts[parity][p].x;
-                    s2 += parts[parity][p].y;
-                }
+                s = norm_join(parts[parity], a.split);
             }
         }
-        const float r = rsqrtf(s1 * invk + a.eps);
-        // in this order c stays in range where r^3 alone does not (r beyond 2^42 or below 2^-42)
-        const float c = r * (s2 * invk) * r * r;
+        // mean x^2 + eps = t 2^(2 (e - 127)), at least 2^-252 (r at most 2^126)
+        const int e = max(max(s.top, a.eps_e), 1);
+        const float g1 = norm_pow2(s.top - e), g2 = norm_pow2(a.eps_e - e);
+        float t = fmaf(s.s1 * invk * g1, g1, a.eps_q * g2 * g2);
+        if (e == 1) t = fmaxf(t, 1.0f);
+        const float rm = rsqrtf(t), r = rm * norm_pow2(127 - e);
+        const float m = s.s2 * g1 * rm * invk;
+        const float xr = rm * norm_pow2(byte - e);  // n = code xr
         if (!active || !mine) continue;
         Bf16x16 o;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float d0 = bf16_lo(cdu.w[k]), d1 = bf16_hi(cdu.w[k]), x0 = x[2 * k], x1 = x[2 * k + 1];
-            acc[2 * k] = fmaf(d0 * x0, r, acc[2 * k]);
-            acc[2 * k + 1] = fmaf(d1 * x1, r, acc[2 * k + 1]);
-            o.w[k] = pack_bf16(fmaf(d0, r * bf16_lo(gain.w[k]), fmaf(-c, x0, bf16_lo(cdr.w[k]))),
-                               fmaf(d1, r * bf16_hi(gain.w[k]), fmaf(-c, x1, bf16_hi(cdr.w[k]))));
+        for (int i = 0; i < 4; ++i) {
+            // decoded again: the values held over the barrier spilled
+            asm volatile("" : "+r"(qw[i]));
+            float y[4];
+            b8_decode4<TYPE>(qw[i], y);
+            float out[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t dw = cdu.w[2 * i + (k >> 1)], gw = gain.w[2 * i + (k >> 1)], rw = cdr.w[2 * i + (k >> 1)];
+                const float d = k & 1 ? bf16_hi(dw) : bf16_lo(dw), n = y[k] * xr;
+                acc[4 * i + k] = fmaf(d, n, acc[4 * i + k]);
+                out[k] = fmaf(r, fmaf(-m, n, d * (k & 1 ? bf16_hi(gw) : bf16_lo(gw))), k & 1 ? bf16_hi(rw) : bf16_lo(rw));
+            }
+            o.w[2 * i] = pack_bf16(out[0], out[1]);
+            o.w[2 * i + 1] = pack_bf16(out[2], out[3]);
         }
         store_bf16x16(a.dX + row * a.K + 16 * ci, o, a.v32);
     }
