@@ -429,8 +429,25 @@ def _ld(t: Optional[torch.Tensor]) -> int:
     return t.size(1) if t.size(0) == 1 else s[0]  # one row has no stride; overlapping rows the library refuses
 
 
+_BF16, _F32, _I8 = torch.bfloat16, torch.float32, torch.int8
+
+
+def _of(t: Optional[torch.Tensor], dtype: torch.dtype):
+    """Address of a tensor of the one element type that the library reads there."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"a {dtype} tensor is needed, not {t.dtype}")
+    return t.data_ptr()
+
+
 def _fp32(t: Optional[torch.Tensor]) -> int:
-    return 1 if t is not None and t.dtype == torch.float32 else 0
+    """1 for fp32, 0 for bf16 (or an absent tensor); the library has no other types here."""
+    if t is None or t.dtype is _BF16:
+        return 0
+    if t.dtype is not _F32:
+        raise ValueError(f"a bfloat16 or float32 tensor is needed, not {t.dtype}")
+    return 1
 
 
 def sbl_b8_row_bytes(d: sbl_b8_desc) -> int:
@@ -460,7 +477,7 @@ def sbl_b8_transpose(d: sbl_b8_desc, src: Block8, out_t: Block8, type_t: Optiona
 
 
 def sbl_b8_dequantize(d: sbl_b8_desc, src: Block8, X: torch.Tensor) -> None:
-    _check(_lib.sbl_b8_dequantize(d, _b8ref(src), _ptr(X), _ld(X), _stream()), "sbl_b8_dequantize")
+    _check(_lib.sbl_b8_dequantize(d, _b8ref(src), _of(X, _BF16), _ld(X), _stream()), "sbl_b8_dequantize")
 
 
 def sbl_b8_gemm(ad: sbl_b8_desc, a: Block8, bd: sbl_b8_desc, b: Block8, D: torch.Tensor, accumulate: bool = False) -> None:
@@ -472,7 +489,7 @@ def sbl_b8_gemm(ad: sbl_b8_desc, a: Block8, bd: sbl_b8_desc, b: Block8, D: torch
 def sbl_b8_linear_forward(wd: sbl_b8_desc, w: Block8, X: torch.Tensor, T: int, xq: Block8, Y: torch.Tensor,
                           x_type: int = SBL_B8_E4M3) -> None:
     """X (bf16) -> its 8-bit form xq (the backward's checkpoint) and Y = xq w^T (bf16 or fp32)."""
-    _check(_lib.sbl_b8_linear_forward(wd, _b8ref(w), _ptr(X), _ld(X), T, x_type, _b8ref(xq), _ptr(Y),
+    _check(_lib.sbl_b8_linear_forward(wd, _b8ref(w), _of(X, _BF16), _ld(X), T, x_type, _b8ref(xq), _ptr(Y),
                                       _ld(Y), _fp32(Y), _stream()), "sbl_b8_linear_forward")
 
 
@@ -485,27 +502,27 @@ def sbl_b8_linear_backward(wd: sbl_b8_desc, w_t: Optional[Block8], xq: Optional[
                            x_type: int = SBL_B8_E4M3, g_type: int = SBL_B8_E4M3, accumulate: bool = False) -> None:
     """dX (bf16 or fp32) and dW (fp32, added to when accumulate) from the checkpoint xq."""
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.sbl_b8_linear_backward(wd, _b8ref(w_t), _b8ref(xq), x_type, _ptr(dY), _ld(dY), T, g_type,
-                                       _ptr(dX), _fp32(dX), _ptr(dW), 1 if accumulate else 0, _ptr(workspace), nbytes,
+    _check(_lib.sbl_b8_linear_backward(wd, _b8ref(w_t), _b8ref(xq), x_type, _of(dY, _BF16), _ld(dY), T, g_type,
+                                       _ptr(dX), _fp32(dX), _of(dW, _F32), 1 if accumulate else 0, _ptr(workspace), nbytes,
                                        _stream()), "sbl_b8_linear_backward")
 
 
 def sbl_glu_forward(d: sbl_b8_desc, act: int, G: torch.Tensor, U: Optional[torch.Tensor], H: Optional[torch.Tensor],
                     g8: Optional[Block8] = None, u8: Optional[Block8] = None) -> None:
     """H = act(G) * U and the checkpoints of G and U; every output optional."""
-    _check(_lib.sbl_glu_forward(d, act, _ptr(G), _ld(G), _ptr(U), _ld(U), _ptr(H), _ld(H), _b8ref(g8),
+    _check(_lib.sbl_glu_forward(d, act, _of(G, _BF16), _ld(G), _of(U, _BF16), _ld(U), _of(H, _BF16), _ld(H), _b8ref(g8),
                                 _b8ref(u8), _stream()), "sbl_glu_forward")
 
 
 def sbl_glu_backward(d: sbl_b8_desc, act: int, g8: Block8, u8: Optional[Block8], dH: torch.Tensor, dG: torch.Tensor,
                      dU: Optional[torch.Tensor]) -> None:
-    _check(_lib.sbl_glu_backward(d, act, _b8ref(g8), _b8ref(u8), _ptr(dH), _ld(dH), _ptr(dG), _ld(dG),
-                                 _ptr(dU), _ld(dU), _stream()), "sbl_glu_backward")
+    _check(_lib.sbl_glu_backward(d, act, _b8ref(g8), _b8ref(u8), _of(dH, _BF16), _ld(dH), _of(dG, _BF16), _ld(dG),
+                                 _of(dU, _BF16), _ld(dU), _stream()), "sbl_glu_backward")
 
 
 def sbl_quantize_act_rmsnorm_checkpoint(d: sbl_b8_desc, X: torch.Tensor, g: Optional[torch.Tensor], eps: float,
                                         Xq: torch.Tensor, dscale: torch.Tensor, x8: Block8) -> None:
-    _check(_lib.sbl_quantize_act_rmsnorm_checkpoint(d, _ptr(X), _ptr(g), float(eps), _ptr(Xq), _ptr(dscale),
+    _check(_lib.sbl_quantize_act_rmsnorm_checkpoint(d, _of(X, _BF16), _of(g, _BF16), float(eps), _of(Xq, _I8), _of(dscale, _F32),
                                                     _b8ref(x8), _stream()), "sbl_quantize_act_rmsnorm_checkpoint")
 
 
@@ -518,8 +535,8 @@ def sbl_rmsnorm_backward(d: sbl_b8_desc, x8: Block8, g: Optional[torch.Tensor], 
                          workspace: Optional[torch.Tensor]) -> None:
     """dX (+ dR) and the gains' gradient dg from the checkpointed norm input x8."""
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.sbl_rmsnorm_backward(d, _b8ref(x8), _ptr(g), float(eps), _ptr(dU), _ptr(dR), _ptr(dX),
-                                     _ptr(dg), _ptr(workspace), nbytes, _stream()), "sbl_rmsnorm_backward")
+    _check(_lib.sbl_rmsnorm_backward(d, _b8ref(x8), _of(g, _BF16), float(eps), _of(dU, _BF16), _of(dR, _BF16), _of(dX, _BF16),
+                                     _of(dg, _F32), _ptr(workspace), nbytes, _stream()), "sbl_rmsnorm_backward")
 
 
 # ------------------------------------------------- allocation helpers (torch)

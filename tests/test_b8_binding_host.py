@@ -1,0 +1,61 @@
+"""What the Python binding of the 8-bit block operators refuses before the library sees a pointer: tensors that the
+C arguments cannot describe.  No device is needed, and none may be present: a call let through would hand host
+pointers to kernels."""
+import pytest
+import torch
+
+T, K, O = 4, 64, 32
+BF, F32, I8 = torch.bfloat16, torch.float32, torch.int8
+
+
+@pytest.fixture(scope="module")
+def sbl():
+    from sparsity_sbl_quantize_b200 import build
+    build.build()
+    from sparsity_sbl_quantize_b200 import sbl as m
+    if torch.cuda.is_available():
+        pytest.skip("a device is present: host pointers must not reach kernels")
+    return m
+
+
+def z(*shape, dtype=BF):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def calls(sbl):
+    """name -> (call taking its tensors, the tensors by name with their type)."""
+    d, wd = sbl.b8_desc(T, K), sbl.b8_desc(O, K)
+    m, w, wt = (sbl.alloc_b8(x, device="cpu") for x in (d, wd, sbl.b8_desc(K, O)))
+    ws = z(1 << 20, dtype=torch.uint8)
+    return {
+        "quantize": (lambda X: sbl.sbl_b8_quantize(d, X, m), {"X": z(T, K)}),
+        "dequantize": (lambda X: sbl.sbl_b8_dequantize(d, m, X), {"X": z(T, K)}),
+        "gemm": (lambda D: sbl.sbl_b8_gemm(d, m, wd, w, D), {"D": z(T, O)}),
+        "linear_forward": (lambda X, Y: sbl.sbl_b8_linear_forward(wd, w, X, T, m, Y), {"X": z(T, K), "Y": z(T, O)}),
+        "linear_backward": (lambda dY, dX, dW: sbl.sbl_b8_linear_backward(wd, wt, m, dY, T, dX, dW, ws),
+                            {"dY": z(T, O), "dX": z(T, K), "dW": z(O, K, dtype=F32)}),
+        "glu_forward": (lambda G, U, H: sbl.sbl_glu_forward(d, 0, G, U, H, m, m), {"G": z(T, K), "U": z(T, K), "H": z(T, K)}),
+        "glu_backward": (lambda dH, dG, dU: sbl.sbl_glu_backward(d, 0, m, m, dH, dG, dU),
+                         {"dH": z(T, K), "dG": z(T, K), "dU": z(T, K)}),
+        "rmsnorm_checkpoint": (lambda X, g, Xq, s: sbl.sbl_quantize_act_rmsnorm_checkpoint(d, X, g, 1e-5, Xq, s, m),
+                               {"X": z(T, K), "g": z(K), "Xq": z(T, K, dtype=I8), "s": z(T, dtype=F32)}),
+        "rmsnorm_backward": (lambda g, dU, dR, dX, dg: sbl.sbl_rmsnorm_backward(d, m, g, 1e-5, dU, dR, dX, dg, ws),
+                             {"g": z(K), "dU": z(T, K), "dR": z(T, K), "dX": z(T, K), "dg": z(K, dtype=F32)}),
+    }
+
+
+EITHER = {("quantize", "X"), ("gemm", "D"), ("linear_forward", "Y"), ("linear_backward", "dX")}  # bf16 or fp32
+ARGUMENTS = [(c, a) for c, names in (
+    ("quantize", "X"), ("dequantize", "X"), ("gemm", "D"), ("linear_forward", "X Y"), ("linear_backward", "dY dX dW"),
+    ("glu_forward", "G U H"), ("glu_backward", "dH dG dU"), ("rmsnorm_checkpoint", "X g Xq s"),
+    ("rmsnorm_backward", "g dU dR dX dg")) for a in names.split()]
+
+
+@pytest.mark.parametrize("call,name", ARGUMENTS)
+def test_other_element_types_are_refused(sbl, call, name):
+    f, args = calls(sbl)[call]
+    right = {BF, F32} if (call, name) in EITHER else {args[name].dtype}
+    for dtype in (torch.float16, torch.float64, torch.int16, torch.uint8, BF, F32, I8):
+        if dtype not in right:
+            with pytest.raises(ValueError, match="tensor is needed"):
+                f(**{**args, name: args[name].to(dtype)})
