@@ -405,6 +405,11 @@ class Block8:
     codes: torch.Tensor
     scales: torch.Tensor
 
+    def __post_init__(self):
+        for t in (self.codes, self.scales):
+            if not t.is_contiguous() or t.element_size() != 1:
+                raise ValueError("codes and scales are contiguous tensors of bytes")
+
     def c(self) -> sbl_b8:
         return sbl_b8(self.codes.data_ptr(), self.scales.data_ptr())
 
@@ -439,6 +444,20 @@ def _of(t: Optional[torch.Tensor], dtype: torch.dtype):
     if t.dtype is not dtype:
         raise ValueError(f"a {dtype} tensor is needed, not {t.dtype}")
     return t.data_ptr()
+
+
+def _flat(t: Optional[torch.Tensor], dtype: torch.dtype):
+    """_of for the arguments that have no row stride in the ABI."""
+    if t is not None and not t.is_contiguous():
+        raise ValueError("a contiguous tensor is needed (this argument has no row stride)")
+    return _of(t, dtype)
+
+
+def _space(workspace: Optional[torch.Tensor]):
+    """Address and bytes of a workspace of any element type."""
+    if workspace is None:
+        return None, 0
+    return _flat(workspace, workspace.dtype), workspace.numel() * workspace.element_size()
 
 
 def _fp32(t: Optional[torch.Tensor]) -> int:
@@ -500,11 +519,11 @@ def sbl_b8_linear_workspace_bytes(wd: sbl_b8_desc, T: int) -> int:
 def sbl_b8_linear_backward(wd: sbl_b8_desc, w_t: Optional[Block8], xq: Optional[Block8], dY: torch.Tensor, T: int,
                            dX: Optional[torch.Tensor], dW: Optional[torch.Tensor], workspace: Optional[torch.Tensor],
                            x_type: int = SBL_B8_E4M3, g_type: int = SBL_B8_E4M3, accumulate: bool = False) -> None:
-    """dX (bf16 or fp32) and dW (fp32, added to when accumulate) from the checkpoint xq."""
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    """dX (bf16 or fp32) and dW (fp32, added to when accumulate), both contiguous, from the checkpoint xq."""
+    dx_fp32 = _fp32(dX)
     _check(_lib.sbl_b8_linear_backward(wd, _b8ref(w_t), _b8ref(xq), x_type, _of(dY, _BF16), _ld(dY), T, g_type,
-                                       _ptr(dX), _fp32(dX), _of(dW, _F32), 1 if accumulate else 0, _ptr(workspace), nbytes,
-                                       _stream()), "sbl_b8_linear_backward")
+                                       _flat(dX, _F32 if dx_fp32 else _BF16), dx_fp32, _flat(dW, _F32), 1 if accumulate else 0,
+                                       *_space(workspace), _stream()), "sbl_b8_linear_backward")
 
 
 def sbl_glu_forward(d: sbl_b8_desc, act: int, G: torch.Tensor, U: Optional[torch.Tensor], H: Optional[torch.Tensor],
@@ -522,7 +541,7 @@ def sbl_glu_backward(d: sbl_b8_desc, act: int, g8: Block8, u8: Optional[Block8],
 
 def sbl_quantize_act_rmsnorm_checkpoint(d: sbl_b8_desc, X: torch.Tensor, g: Optional[torch.Tensor], eps: float,
                                         Xq: torch.Tensor, dscale: torch.Tensor, x8: Block8) -> None:
-    _check(_lib.sbl_quantize_act_rmsnorm_checkpoint(d, _of(X, _BF16), _of(g, _BF16), float(eps), _of(Xq, _I8), _of(dscale, _F32),
+    _check(_lib.sbl_quantize_act_rmsnorm_checkpoint(d, _flat(X, _BF16), _flat(g, _BF16), float(eps), _flat(Xq, _I8), _flat(dscale, _F32),
                                                     _b8ref(x8), _stream()), "sbl_quantize_act_rmsnorm_checkpoint")
 
 
@@ -534,9 +553,8 @@ def sbl_rmsnorm_backward(d: sbl_b8_desc, x8: Block8, g: Optional[torch.Tensor], 
                          dR: Optional[torch.Tensor], dX: torch.Tensor, dg: Optional[torch.Tensor],
                          workspace: Optional[torch.Tensor]) -> None:
     """dX (+ dR) and the gains' gradient dg from the checkpointed norm input x8."""
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.sbl_rmsnorm_backward(d, _b8ref(x8), _of(g, _BF16), float(eps), _of(dU, _BF16), _of(dR, _BF16), _of(dX, _BF16),
-                                     _of(dg, _F32), _ptr(workspace), nbytes, _stream()), "sbl_rmsnorm_backward")
+    _check(_lib.sbl_rmsnorm_backward(d, _b8ref(x8), _flat(g, _BF16), float(eps), _flat(dU, _BF16), _flat(dR, _BF16), _flat(dX, _BF16),
+                                     _flat(dg, _F32), *_space(workspace), _stream()), "sbl_rmsnorm_backward")
 
 
 # ------------------------------------------------- allocation helpers (torch)

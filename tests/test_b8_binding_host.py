@@ -59,3 +59,41 @@ def test_other_element_types_are_refused(sbl, call, name):
         if dtype not in right:
             with pytest.raises(ValueError, match="tensor is needed"):
                 f(**{**args, name: args[name].to(dtype)})
+
+
+STRIDED = {("quantize", "X"), ("dequantize", "X"), ("gemm", "D"), ("linear_forward", "X"), ("linear_forward", "Y"), ("linear_backward", "dY"),
+           ("glu_forward", "G"), ("glu_forward", "U"), ("glu_forward", "H"), ("glu_backward", "dH"), ("glu_backward", "dG"),
+           ("glu_backward", "dU")}  # these have a row stride in the ABI
+
+
+@pytest.mark.parametrize("call,name", [x for x in ARGUMENTS if x not in STRIDED])
+def test_slices_of_wider_buffers_are_refused_where_there_is_no_stride(sbl, call, name):
+    f, args = calls(sbl)[call]
+    t = args[name]
+    wide = torch.zeros(*t.shape[:-1], 2 * t.shape[-1], dtype=t.dtype)
+    for bad in (wide[..., :t.shape[-1]], wide[..., ::2]):
+        if bad.is_contiguous():
+            continue  # the first half of a vector
+        with pytest.raises(ValueError, match="contiguous"):
+            f(**{**args, name: bad})
+
+
+@pytest.mark.parametrize("call,name", sorted(STRIDED))
+def test_rows_themselves_have_to_be_contiguous(sbl, call, name):
+    f, args = calls(sbl)[call]
+    t = args[name]
+    with pytest.raises(ValueError, match="contiguous rows"):
+        f(**{**args, name: torch.zeros(t.shape[0], 2 * t.shape[1], dtype=t.dtype)[:, ::2]})
+
+
+def test_workspaces_and_stored_matrices_are_contiguous(sbl):
+    d, wd = sbl.b8_desc(T, K), sbl.b8_desc(O, K)
+    m = sbl.alloc_b8(d, device="cpu")
+    gaps = torch.zeros(1 << 21, dtype=torch.uint8)[::2]
+    with pytest.raises(ValueError, match="contiguous"):
+        sbl.sbl_b8_linear_backward(wd, None, m, z(T, O), T, None, z(O, K, dtype=F32), gaps)
+    with pytest.raises(ValueError, match="contiguous"):
+        sbl.sbl_rmsnorm_backward(d, m, z(K), 1e-5, z(T, K), None, z(T, K), z(K, dtype=F32), gaps)
+    for codes, scales in ((torch.zeros(T, 2 * K, dtype=torch.uint8)[:, :K], m.scales), (m.codes, gaps), (m.codes.short(), m.scales)):
+        with pytest.raises(ValueError, match="contiguous tensors of bytes"):
+            sbl.Block8(codes=codes, scales=scales)
