@@ -207,12 +207,17 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+# torch's own queries of the current device and its stream: 0.3 us together, where building a torch.cuda.Stream costs
+# 3.4, half of a small call.  They are not public names: where a torch lacks them the public ones serve.
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    """torch's current stream as a cudaStream_t.  The raw query costs 0.3 us
-    where building a torch.cuda.Stream costs 3.4, half of a small call."""
-    if torch.cuda.is_initialized():
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return torch.cuda.current_stream().cuda_stream  # initialises CUDA, or raises
+    """torch's current stream as a cudaStream_t."""
+    if _raw_device is None or _raw_stream is None or not torch.cuda.is_initialized():
+        return torch.cuda.current_stream().cuda_stream  # initialises CUDA, or raises
+    return _raw_stream(_raw_device())
 
 
 def desc(out_features: int, in_features: int, n: int, m: int) -> sbl_layer_desc:

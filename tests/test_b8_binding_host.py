@@ -97,3 +97,17 @@ def test_workspaces_and_stored_matrices_are_contiguous(sbl):
     for codes, scales in ((torch.zeros(T, 2 * K, dtype=torch.uint8)[:, :K], m.scales), (m.codes, gaps), (m.codes.short(), m.scales)):
         with pytest.raises(ValueError, match="contiguous tensors of bytes"):
             sbl.Block8(codes=codes, scales=scales)
+
+
+@pytest.mark.parametrize("missing", ["_raw_device", "_raw_stream"])
+def test_stream_without_torchs_private_names(sbl, monkeypatch, missing):
+    class Stream:
+        cuda_stream = 0x5EED
+
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    monkeypatch.setattr(sbl, "_raw_device", lambda: 3)
+    monkeypatch.setattr(sbl, "_raw_stream", lambda d: 0x1000 + d)
+    assert sbl._stream() == 0x1003
+    monkeypatch.setattr(sbl, missing, None)
+    assert sbl._stream() == 0x5EED
