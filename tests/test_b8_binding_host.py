@@ -111,3 +111,57 @@ def test_stream_without_torchs_private_names(sbl, monkeypatch, missing):
     assert sbl._stream() == 0x1003
     monkeypatch.setattr(sbl, missing, None)
     assert sbl._stream() == 0x5EED
+
+
+@pytest.mark.parametrize("call", sorted({c for c, _ in ARGUMENTS}))
+def test_host_tensors_are_refused(sbl, call):
+    f, args = calls(sbl)[call]
+    with pytest.raises(ValueError, match="device"):
+        f(**args)
+
+
+@pytest.mark.parametrize("call,name", ARGUMENTS)
+def test_tensors_of_another_device_are_refused(sbl, call, name, monkeypatch):
+    """Every tensor on device 0 but one: the calls that name it are refused, and only those reach the stream."""
+    f, args = calls(sbl)[call]
+    odd = args[name]
+
+    class Reached(Exception):
+        pass
+
+    def stream(device):
+        raise Reached
+
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(sbl, "_raw_device", lambda: 0)
+    monkeypatch.setattr(sbl, "_raw_stream", stream)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 1 if self is odd else 0)
+    with pytest.raises(ValueError, match="a tensor of device 1"):
+        f(**args)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    with pytest.raises(Reached):
+        f(**args)
+
+
+def test_stored_matrices_of_another_device_are_refused(sbl, monkeypatch):
+    d, wd = sbl.b8_desc(T, K), sbl.b8_desc(O, K)
+    m, w, wt = (sbl.alloc_b8(x, device="cpu") for x in (d, wd, sbl.b8_desc(K, O)))
+    with pytest.raises(ValueError, match="one device"):
+        sbl.Block8(codes=m.codes, scales=m.scales.to("meta"))
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(sbl, "_raw_device", lambda: 0)
+    for odd in (m, w, wt):
+        monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 1 if self is odd.codes else 0)
+        with pytest.raises(ValueError, match="a tensor of device 1"):
+            if odd is wt:
+                sbl.sbl_b8_linear_backward(wd, wt, m, z(T, O), T, z(T, K), None, z(1 << 20))
+            else:
+                sbl.sbl_b8_linear_forward(wd, w, z(T, K), T, m, z(T, O))
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 1 if self is m.codes else 0)
+    for f in (lambda: sbl.sbl_b8_transpose(d, w, m), lambda: sbl.sbl_b8_transpose(d, m, w), lambda: sbl.sbl_b8_dequantize(d, m, z(T, K)),
+              lambda: sbl.sbl_b8_quantize(d, z(T, K), None, m), lambda: sbl.sbl_b8_gemm(d, m, wd, w, z(T, O)),
+              lambda: sbl.sbl_glu_forward(d, 0, z(T, K), z(T, K), None, w, m), lambda: sbl.sbl_glu_backward(d, 0, w, m, z(T, K), z(T, K), z(T, K)),
+              lambda: sbl.sbl_quantize_act_rmsnorm_checkpoint(d, z(T, K), None, 0.0, z(T, K, dtype=I8), z(T, dtype=F32), m),
+              lambda: sbl.sbl_rmsnorm_backward(d, m, None, 0.0, z(T, K), None, z(T, K), None, None)):
+        with pytest.raises(ValueError, match="a tensor of device 1"):
+            f()
