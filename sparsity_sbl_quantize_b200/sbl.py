@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -156,7 +157,7 @@ _lib.sbl_container_info.restype = ctypes.c_int
 _lib.sbl_container_info.argtypes = [_P, _sz, _D, ctypes.POINTER(_u32), ctypes.POINTER(ctypes.c_float)]
 _lib.sbl_container_read.restype = ctypes.c_int
 _lib.sbl_container_read.argtypes = [_P, _sz, ctypes.POINTER(sbl_host_buffers)]
-_B, _M = ctypes.POINTER(sbl_b8_desc), ctypes.POINTER(sbl_b8)
+_B, _M = ctypes.POINTER(sbl_b8_desc), ctypes.c_void_p
 _i64 = ctypes.c_int64
 for _name, _args in {
         "sbl_b8_quantize": [_B, _P, _i32, _i64, ctypes.c_int, _M, _M, _P],
@@ -428,8 +429,12 @@ def b8_desc(rows: int, cols: int, type: int = SBL_B8_E4M3) -> sbl_b8_desc:
     return sbl_b8_desc(rows, cols, type)
 
 
+_pack_b8 = struct.Struct("PP").pack
+
+
 def _b8ref(m: Optional[Block8]):
-    return None if m is None else sbl_b8(m.codes.data_ptr(), m.scales.data_ptr())
+    """The bytes of an sbl_b8, which ctypes passes by address (0.1 us; building the structure takes 0.3)."""
+    return None if m is None else _pack_b8(m.codes.data_ptr(), m.scales.data_ptr())
 
 
 def _ld(t: Optional[torch.Tensor]) -> int:
