@@ -214,6 +214,10 @@ _raw_device = getattr(torch._C, "_cuda_getDevice", None)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+def _device() -> int:
+    return torch.cuda.current_device() if _raw_device is None else _raw_device()
+
+
 def _stream():
     """torch's current stream as a cudaStream_t."""
     if _raw_device is None or _raw_stream is None or not torch.cuda.is_initialized():
@@ -418,9 +422,6 @@ class Block8:
         if self.codes.device != self.scales.device:
             raise ValueError("codes and scales lie on one device")
 
-    def get_device(self) -> int:
-        return self.codes.get_device()
-
     def c(self) -> sbl_b8:
         return sbl_b8(self.codes.data_ptr(), self.scales.data_ptr())
 
@@ -452,15 +453,17 @@ def _ld(t: Optional[torch.Tensor]) -> int:
 _BF16, _F32, _I8 = torch.bfloat16, torch.float32, torch.int8
 
 
-def _here(*args):
-    """The current stream, for tensors and stored matrices that all lie on the current device: on another one (or on
-    the host) the kernels would follow the pointers into memory that is not theirs, ordered by no stream."""
-    dev = None  # before CUDA's initialisation no tensor is on a device
-    if torch.cuda.is_initialized():
-        dev = torch.cuda.current_device() if _raw_device is None else _raw_device()
-    for t in args:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor of device {t.get_device()} (-1: the host) was given where device {dev} is current")
+def _here(*tensors):
+    """The current stream, for tensors that all lie on the current device: on another one (or on the host) the kernels
+    would follow the pointers into memory that is not theirs, ordered by no stream."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            own = t.get_device()
+            if own != dev:
+                if dev is not None or own < 0 or own != _device():
+                    raise ValueError(f"a tensor of device {own} (-1: the host) was given where another device is current")
+                dev = own
     return _stream() if dev is None or _raw_stream is None else _raw_stream(dev)
 
 
@@ -513,30 +516,30 @@ def alloc_b8(d: sbl_b8_desc, device="cuda") -> Block8:
 def sbl_b8_quantize(d: sbl_b8_desc, X: torch.Tensor, out: Optional[Block8], out_t: Optional[Block8] = None,
                     blocks: int = SBL_B8_ROWS) -> None:
     """X (bf16 or fp32, any row stride) -> out and / or its transpose out_t."""
-    _check(_lib.sbl_b8_quantize(d, _ptr(X), _fp32(X), _ld(X), blocks, _b8ref(out), _b8ref(out_t), _here(X, out, out_t)),
-           "sbl_b8_quantize")
+    _check(_lib.sbl_b8_quantize(d, _ptr(X), _fp32(X), _ld(X), blocks, _b8ref(out), _b8ref(out_t),
+                                _here(X, out and out.codes, out_t and out_t.codes)), "sbl_b8_quantize")
 
 
 def sbl_b8_transpose(d: sbl_b8_desc, src: Block8, out_t: Block8, type_t: Optional[int] = None) -> None:
     _check(_lib.sbl_b8_transpose(d, _b8ref(src), d.type if type_t is None else type_t, _b8ref(out_t),
-                                 _here(src, out_t)), "sbl_b8_transpose")
+                                 _here(src and src.codes, out_t and out_t.codes)), "sbl_b8_transpose")
 
 
 def sbl_b8_dequantize(d: sbl_b8_desc, src: Block8, X: torch.Tensor) -> None:
-    _check(_lib.sbl_b8_dequantize(d, _b8ref(src), _of(X, _BF16), _ld(X), _here(src, X)), "sbl_b8_dequantize")
+    _check(_lib.sbl_b8_dequantize(d, _b8ref(src), _of(X, _BF16), _ld(X), _here(src and src.codes, X)), "sbl_b8_dequantize")
 
 
 def sbl_b8_gemm(ad: sbl_b8_desc, a: Block8, bd: sbl_b8_desc, b: Block8, D: torch.Tensor, accumulate: bool = False) -> None:
     """D [a rows, b rows] (bf16 or fp32) = or += a b^T."""
     _check(_lib.sbl_b8_gemm(ad, _b8ref(a), bd, _b8ref(b), _ptr(D), _ld(D), _fp32(D),
-                            1 if accumulate else 0, _here(a, b, D)), "sbl_b8_gemm")
+                            1 if accumulate else 0, _here(a and a.codes, b and b.codes, D)), "sbl_b8_gemm")
 
 
 def sbl_b8_linear_forward(wd: sbl_b8_desc, w: Block8, X: torch.Tensor, T: int, xq: Block8, Y: torch.Tensor,
                           x_type: int = SBL_B8_E4M3) -> None:
     """X (bf16) -> its 8-bit form xq (the backward's checkpoint) and Y = xq w^T (bf16 or fp32)."""
     _check(_lib.sbl_b8_linear_forward(wd, _b8ref(w), _of(X, _BF16), _ld(X), T, x_type, _b8ref(xq), _ptr(Y),
-                                      _ld(Y), _fp32(Y), _here(w, X, xq, Y)), "sbl_b8_linear_forward")
+                                      _ld(Y), _fp32(Y), _here(w and w.codes, X, xq and xq.codes, Y)), "sbl_b8_linear_forward")
 
 
 def sbl_b8_linear_workspace_bytes(wd: sbl_b8_desc, T: int) -> int:
@@ -550,26 +553,27 @@ def sbl_b8_linear_backward(wd: sbl_b8_desc, w_t: Optional[Block8], xq: Optional[
     dx_fp32 = _fp32(dX)
     _check(_lib.sbl_b8_linear_backward(wd, _b8ref(w_t), _b8ref(xq), x_type, _of(dY, _BF16), _ld(dY), T, g_type,
                                        _flat(dX, _F32 if dx_fp32 else _BF16), dx_fp32, _flat(dW, _F32), 1 if accumulate else 0,
-                                       *_space(workspace), _here(w_t, xq, dY, dX, dW, workspace)), "sbl_b8_linear_backward")
+                                       *_space(workspace), _here(w_t and w_t.codes, xq and xq.codes, dY, dX, dW, workspace)),
+           "sbl_b8_linear_backward")
 
 
 def sbl_glu_forward(d: sbl_b8_desc, act: int, G: torch.Tensor, U: Optional[torch.Tensor], H: Optional[torch.Tensor],
                     g8: Optional[Block8] = None, u8: Optional[Block8] = None) -> None:
     """H = act(G) * U and the checkpoints of G and U; every output optional."""
     _check(_lib.sbl_glu_forward(d, act, _of(G, _BF16), _ld(G), _of(U, _BF16), _ld(U), _of(H, _BF16), _ld(H), _b8ref(g8),
-                                _b8ref(u8), _here(G, U, H, g8, u8)), "sbl_glu_forward")
+                                _b8ref(u8), _here(G, U, H, g8 and g8.codes, u8 and u8.codes)), "sbl_glu_forward")
 
 
 def sbl_glu_backward(d: sbl_b8_desc, act: int, g8: Block8, u8: Optional[Block8], dH: torch.Tensor, dG: torch.Tensor,
                      dU: Optional[torch.Tensor]) -> None:
     _check(_lib.sbl_glu_backward(d, act, _b8ref(g8), _b8ref(u8), _of(dH, _BF16), _ld(dH), _of(dG, _BF16), _ld(dG),
-                                 _of(dU, _BF16), _ld(dU), _here(g8, u8, dH, dG, dU)), "sbl_glu_backward")
+                                 _of(dU, _BF16), _ld(dU), _here(g8 and g8.codes, u8 and u8.codes, dH, dG, dU)), "sbl_glu_backward")
 
 
 def sbl_quantize_act_rmsnorm_checkpoint(d: sbl_b8_desc, X: torch.Tensor, g: Optional[torch.Tensor], eps: float,
                                         Xq: torch.Tensor, dscale: torch.Tensor, x8: Block8) -> None:
     _check(_lib.sbl_quantize_act_rmsnorm_checkpoint(d, _flat(X, _BF16), _flat(g, _BF16), float(eps), _flat(Xq, _I8), _flat(dscale, _F32),
-                                                    _b8ref(x8), _here(X, g, Xq, dscale, x8)), "sbl_quantize_act_rmsnorm_checkpoint")
+                                                    _b8ref(x8), _here(X, g, Xq, dscale, x8 and x8.codes)), "sbl_quantize_act_rmsnorm_checkpoint")
 
 
 def sbl_rmsnorm_backward_workspace_bytes(T: int, K: int) -> int:
@@ -581,7 +585,7 @@ def sbl_rmsnorm_backward(d: sbl_b8_desc, x8: Block8, g: Optional[torch.Tensor], 
                          workspace: Optional[torch.Tensor]) -> None:
     """dX (+ dR) and the gains' gradient dg from the checkpointed norm input x8."""
     _check(_lib.sbl_rmsnorm_backward(d, _b8ref(x8), _flat(g, _BF16), float(eps), _flat(dU, _BF16), _flat(dR, _BF16), _flat(dX, _BF16),
-                                     _flat(dg, _F32), *_space(workspace), _here(x8, g, dU, dR, dX, dg, workspace)), "sbl_rmsnorm_backward")
+                                     _flat(dg, _F32), *_space(workspace), _here(x8 and x8.codes, g, dU, dR, dX, dg, workspace)), "sbl_rmsnorm_backward")
 
 
 # ------------------------------------------------- allocation helpers (torch)
