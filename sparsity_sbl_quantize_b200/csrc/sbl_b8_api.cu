@@ -462,7 +462,11 @@ static sbl_status gemm(const HostDevice &hd, const sbl_b8_desc *ad, const sbl_b8
         return ((static_cast<int64_t>(args.M) + kBM - 1) / kBM * ((args.N + bn - 1) / bn) + hd.num_sms - 1) / hd.num_sms;
     };
     const bool wide = 460 + rounds(256) * (42ll * args.k_blocks + 60) <= 340 + rounds(128) * (34ll * args.k_blocks + 45);
-    const bool lng = fp32 && args.k_blocks > kB8SegBlocks;
+    // bf16 results of a very long K are summed in segments too: over products of
+    // one sign the tensor core's truncation reaches 2^-23 of the sum every 32 of K,
+    // at 65536 a sixteenth of the half step (600000: off by one step in places),
+    // and one accumulator over all of K would outlast the epilogue's wait
+    const bool lng = args.k_blocks > (fp32 ? kB8SegBlocks : kB8MaxBf16Blocks);
     if (wide)
         return lng ? launch_b8_gemm<256, true>(hd, ad, A, bd, B, D, ldd, args, stream)
                    : launch_b8_gemm<256, false>(hd, ad, A, bd, B, D, ldd, args, stream);

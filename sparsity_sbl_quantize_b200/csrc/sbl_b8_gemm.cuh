@@ -152,8 +152,10 @@ __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap *map, uint32
 
 // K blocks summed in tensor memory before the sum moves to registers (LONG).
 constexpr int kB8SegBlocks = 32;
+// K blocks of a bf16 result from which it is summed so as well.
+constexpr int kB8MaxBf16Blocks = 512;
 
-// LONG: fp32 results of long reductions.  The tensor core truncates when it
+// LONG: results of long reductions, fp32 ones above all.  The tensor core truncates when it
 // adds to its accumulator, so the error of a sum of n steps grows with n
 // (relative to the result, measured on random operands: 1.0e-7 at K = 2048,
 // 4.8e-7 at 8192, 1.2e-6 at 16384, where rounded additions give 1.9e-7).  The
