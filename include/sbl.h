@@ -590,6 +590,10 @@ sbl_status sbl_b8_gemm(const sbl_b8_desc *a_desc, const sbl_b8 *a, const sbl_b8_
 /* A linear layer on b8 operands, for the linears a model does not ternarise.
  * W [O, K]: w_desc = {O, K, type}, O and K multiples of 16 up to 65536;
  * usually quantised with SBL_B8_TILES, whose transposed output is w_t below.
+ * A larger O (a head over a large vocabulary) is one linear per slab of at most
+ * 65536 rows of W: Y and dY of a slab are columns of the whole ones, its dW rows
+ * of the whole dW, and the slabs' dX (fp32) add up.  With slabs of a multiple of
+ * 128 rows every block of the quantisers is that of the undivided matrix.
  * Forward: xq = X [T, K] (bf16, row stride ldx) quantised along rows, an
  * output that is at once the product's operand and the checkpoint the
  * backward reads; Y [T, O] = xq w^T (bf16 or fp32, row stride ldy). */

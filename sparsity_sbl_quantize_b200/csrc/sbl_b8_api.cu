@@ -59,8 +59,9 @@ static sbl_status b8_device(HostDevice *hd)
     return SBL_OK;
 }
 
-// Launch with programmatic dependent launch: every kernel here waits for the
-// one before it (griddepcontrol.wait) before it touches global memory.
+// Launch with programmatic dependent launch: a kernel waits for the one before
+// it (griddepcontrol.wait) before it touches global memory, or, one that neither
+// reads nor writes what the one before it writes (`late`), before it ends.
 template <typename... P, typename... A>
 static sbl_status launch2(void (*kernel)(P...), int64_t grid, int64_t grid_y, int block, size_t smem, cudaStream_t stream, A... args)
 {
@@ -705,9 +706,10 @@ sbl_status sbl_b8_linear_forward(const sbl_b8_desc *w_desc, const sbl_b8 *w, con
     if ((st = b8_device(&hd)) != SBL_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // One launch that quantises X itself while each CTA's share of it is
-    // small: about 112 (token, block) pairs measured even with two launches
-    // (6912 x 2560: 1 token 7.3 us against 9.1, 16 tokens, 80 pairs, 8.5 against 9.8,
-    // 24 tokens 10.4 against 10.2; 2560 x 6912: 16 tokens, 112 pairs, 9.6 against 10.6).
+    // small, up to 112 (token, block) pairs; 120 measured even with two launches
+    // (6912 x 2560: 1 token, 5 pairs, 7.3 us against 9.1, 16 tokens, 80 pairs, 8.5
+    // against 9.8, 24 tokens, 120 pairs, 10.4 against 10.2; 2560 x 6912: 16 tokens,
+    // 112 pairs, 9.6 against 10.6).
     if (T <= 64) {
         const SkinnyPlan p = skinny_plan(hd.num_sms, w_desc->rows, w_desc->cols, T, true);
         if (p.smem <= kB8SmemAll && p.tmem_cols <= kTmemCols && static_cast<int64_t>(T) * p.max_blocks <= 112 && !(y_is_fp32 && p.max_blocks > kB8SegBlocks))

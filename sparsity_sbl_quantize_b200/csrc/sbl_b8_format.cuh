@@ -30,8 +30,10 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // Round-half-even of |v| < 2^22 by the fp32 adder: fl(v + 1.5 2^23) has ulp 1
 // and lies in [2^23, 2^24), so its bits are 0x4B400000 + rint(v), and the low
 // byte is rint(v) as an int8 bit pattern when rint(v) is in [-128, 127].  The
-// quantiser's products satisfy |fl32(x fl32(127 / a))| <= 127 (1 + 2^-24) for
-// |x| <= a, so rint lies in [-127, 127] and the clamp to [-128, 127] never
+// quantisers' products are at most 127 but for their roundings, for |x| <= a:
+// |fl32(x fl32(127 / a))| <= 127 (1 + 2^-24)^2, with the checkpointed norm's
+// factor |fl32(x fl32(127 fl32(1 / a)))| <= 127 (1 + 2^-24)^3, and a b8 int8 code's
+// x 2^-e is exact.  So rint lies in [-127, 127] and the clamp to [-128, 127] never
 // binds; one FADD replaces the float-to-int conversion.
 __device__ __forceinline__ uint32_t rne_byte(float v)
 {
