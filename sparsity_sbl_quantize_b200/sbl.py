@@ -208,21 +208,15 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-# torch's own queries of the current device and its stream: 0.3 us together, where building a torch.cuda.Stream costs
-# 3.4, half of a small call.  They are not public names: where a torch lacks them the public ones serve.
-_raw_device = getattr(torch._C, "_cuda_getDevice", None)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _device() -> int:
-    return torch.cuda.current_device() if _raw_device is None else _raw_device()
+# The current device and its stream.  torch's own queries take 0.3 us together, where building a torch.cuda.Stream takes
+# 3.4, half of a small call; they are not public names, so where a torch lacks them the public ones serve.
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _stream():
-    """torch's current stream as a cudaStream_t."""
-    if _raw_device is None or _raw_stream is None or not torch.cuda.is_initialized():
-        return torch.cuda.current_stream().cuda_stream  # initialises CUDA, or raises
-    return _raw_stream(_raw_device())
+    """torch's current stream as a cudaStream_t (initialises CUDA, or raises)."""
+    return _stream_of(_device())
 
 
 def desc(out_features: int, in_features: int, n: int, m: int) -> sbl_layer_desc:
@@ -430,12 +424,47 @@ def b8_desc(rows: int, cols: int, type: int = SBL_B8_E4M3) -> sbl_b8_desc:
     return sbl_b8_desc(rows, cols, type)
 
 
+_BF16, _F32, _I8 = torch.bfloat16, torch.float32, torch.int8
 _pack_b8 = struct.Struct("PP").pack
 
+# The arguments of a call, each checked against what the library will make of its pointer: the element type, the
+# current device `dev` (on another one, or the host, the kernels would follow the pointer into memory that is not theirs,
+# ordered by no stream) and, where the ABI has no row stride, contiguity.  A tenth of a microsecond a tensor.
 
-def _b8ref(m: Optional[Block8]):
+
+def _refuse(t: torch.Tensor, dtype: torch.dtype, dev: int):
+    if t.dtype is not dtype:
+        raise ValueError(f"a {dtype} tensor is needed, not {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"a tensor of device {t.get_device()} (-1: the host) was given where device {dev} is current")
+    raise ValueError("a contiguous tensor is needed (this argument has no row stride)")
+
+
+def _rows(t: Optional[torch.Tensor], dtype: torch.dtype, dev: int):
+    """Address of a matrix that is passed with its row stride (_ld)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, dtype, dev)
+    return t.data_ptr()
+
+
+def _flat(t: Optional[torch.Tensor], dtype: Optional[torch.dtype], dev: int):
+    """Address of a contiguous tensor (dtype None: of any type)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype and dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dtype or t.dtype, dev)
+    return t.data_ptr()
+
+
+def _b8ref(m: Optional[Block8], dev: int):
     """The bytes of an sbl_b8, which ctypes passes by address (0.1 us; building the structure takes 0.3)."""
-    return None if m is None else _pack_b8(m.codes.data_ptr(), m.scales.data_ptr())
+    if m is None:
+        return None
+    if m.codes.get_device() != dev:
+        _refuse(m.codes, m.codes.dtype, dev)
+    return _pack_b8(m.codes.data_ptr(), m.scales.data_ptr())
 
 
 def _ld(t: Optional[torch.Tensor]) -> int:
@@ -450,53 +479,13 @@ def _ld(t: Optional[torch.Tensor]) -> int:
     return t.size(1) if t.size(0) == 1 else s[0]  # one row has no stride; overlapping rows the library refuses
 
 
-_BF16, _F32, _I8 = torch.bfloat16, torch.float32, torch.int8
-
-
-def _here(*tensors):
-    """The current stream, for tensors that all lie on the current device: on another one (or on the host) the kernels
-    would follow the pointers into memory that is not theirs, ordered by no stream."""
-    dev = None
-    for t in tensors:
-        if t is not None:
-            own = t.get_device()
-            if own != dev:
-                if dev is not None or own < 0 or own != _device():
-                    raise ValueError(f"a tensor of device {own} (-1: the host) was given where another device is current")
-                dev = own
-    return _stream() if dev is None or _raw_stream is None else _raw_stream(dev)
-
-
-def _of(t: Optional[torch.Tensor], dtype: torch.dtype):
-    """Address of a tensor of the one element type that the library reads there."""
-    if t is None:
-        return None
-    if t.dtype is not dtype:
-        raise ValueError(f"a {dtype} tensor is needed, not {t.dtype}")
-    return t.data_ptr()
-
-
-def _flat(t: Optional[torch.Tensor], dtype: torch.dtype):
-    """_of for the arguments that have no row stride in the ABI."""
-    if t is not None and not t.is_contiguous():
-        raise ValueError("a contiguous tensor is needed (this argument has no row stride)")
-    return _of(t, dtype)
-
-
-def _space(workspace: Optional[torch.Tensor]):
-    """Address and bytes of a workspace of any element type."""
-    if workspace is None:
-        return None, 0
-    return _flat(workspace, workspace.dtype), workspace.numel() * workspace.element_size()
-
-
-def _fp32(t: Optional[torch.Tensor]) -> int:
-    """1 for fp32, 0 for bf16 (or an absent tensor); the library has no other types here."""
+def _float(t: Optional[torch.Tensor]) -> torch.dtype:
+    """The type of a tensor that may be fp32 or bf16 (bf16 of an absent one)."""
     if t is None or t.dtype is _BF16:
-        return 0
+        return _BF16
     if t.dtype is not _F32:
         raise ValueError(f"a bfloat16 or float32 tensor is needed, not {t.dtype}")
-    return 1
+    return _F32
 
 
 def sbl_b8_row_bytes(d: sbl_b8_desc) -> int:
@@ -516,30 +505,35 @@ def alloc_b8(d: sbl_b8_desc, device="cuda") -> Block8:
 def sbl_b8_quantize(d: sbl_b8_desc, X: torch.Tensor, out: Optional[Block8], out_t: Optional[Block8] = None,
                     blocks: int = SBL_B8_ROWS) -> None:
     """X (bf16 or fp32, any row stride) -> out and / or its transpose out_t."""
-    _check(_lib.sbl_b8_quantize(d, _ptr(X), _fp32(X), _ld(X), blocks, _b8ref(out), _b8ref(out_t),
-                                _here(X, out and out.codes, out_t and out_t.codes)), "sbl_b8_quantize")
+    dev, x = _device(), _float(X)
+    _check(_lib.sbl_b8_quantize(d, _rows(X, x, dev), 1 if x is _F32 else 0, _ld(X), blocks, _b8ref(out, dev), _b8ref(out_t, dev),
+                                _stream_of(dev)), "sbl_b8_quantize")
 
 
 def sbl_b8_transpose(d: sbl_b8_desc, src: Block8, out_t: Block8, type_t: Optional[int] = None) -> None:
-    _check(_lib.sbl_b8_transpose(d, _b8ref(src), d.type if type_t is None else type_t, _b8ref(out_t),
-                                 _here(src and src.codes, out_t and out_t.codes)), "sbl_b8_transpose")
+    dev = _device()
+    _check(_lib.sbl_b8_transpose(d, _b8ref(src, dev), d.type if type_t is None else type_t, _b8ref(out_t, dev),
+                                 _stream_of(dev)), "sbl_b8_transpose")
 
 
 def sbl_b8_dequantize(d: sbl_b8_desc, src: Block8, X: torch.Tensor) -> None:
-    _check(_lib.sbl_b8_dequantize(d, _b8ref(src), _of(X, _BF16), _ld(X), _here(src and src.codes, X)), "sbl_b8_dequantize")
+    dev = _device()
+    _check(_lib.sbl_b8_dequantize(d, _b8ref(src, dev), _rows(X, _BF16, dev), _ld(X), _stream_of(dev)), "sbl_b8_dequantize")
 
 
 def sbl_b8_gemm(ad: sbl_b8_desc, a: Block8, bd: sbl_b8_desc, b: Block8, D: torch.Tensor, accumulate: bool = False) -> None:
     """D [a rows, b rows] (bf16 or fp32) = or += a b^T."""
-    _check(_lib.sbl_b8_gemm(ad, _b8ref(a), bd, _b8ref(b), _ptr(D), _ld(D), _fp32(D),
-                            1 if accumulate else 0, _here(a and a.codes, b and b.codes, D)), "sbl_b8_gemm")
+    dev, out = _device(), _float(D)
+    _check(_lib.sbl_b8_gemm(ad, _b8ref(a, dev), bd, _b8ref(b, dev), _rows(D, out, dev), _ld(D), 1 if out is _F32 else 0,
+                            1 if accumulate else 0, _stream_of(dev)), "sbl_b8_gemm")
 
 
 def sbl_b8_linear_forward(wd: sbl_b8_desc, w: Block8, X: torch.Tensor, T: int, xq: Block8, Y: torch.Tensor,
                           x_type: int = SBL_B8_E4M3) -> None:
     """X (bf16) -> its 8-bit form xq (the backward's checkpoint) and Y = xq w^T (bf16 or fp32)."""
-    _check(_lib.sbl_b8_linear_forward(wd, _b8ref(w), _of(X, _BF16), _ld(X), T, x_type, _b8ref(xq), _ptr(Y),
-                                      _ld(Y), _fp32(Y), _here(w and w.codes, X, xq and xq.codes, Y)), "sbl_b8_linear_forward")
+    dev, y = _device(), _float(Y)
+    _check(_lib.sbl_b8_linear_forward(wd, _b8ref(w, dev), _rows(X, _BF16, dev), _ld(X), T, x_type, _b8ref(xq, dev), _rows(Y, y, dev),
+                                      _ld(Y), 1 if y is _F32 else 0, _stream_of(dev)), "sbl_b8_linear_forward")
 
 
 def sbl_b8_linear_workspace_bytes(wd: sbl_b8_desc, T: int) -> int:
@@ -550,30 +544,34 @@ def sbl_b8_linear_backward(wd: sbl_b8_desc, w_t: Optional[Block8], xq: Optional[
                            dX: Optional[torch.Tensor], dW: Optional[torch.Tensor], workspace: Optional[torch.Tensor],
                            x_type: int = SBL_B8_E4M3, g_type: int = SBL_B8_E4M3, accumulate: bool = False) -> None:
     """dX (bf16 or fp32) and dW (fp32, added to when accumulate), both contiguous, from the checkpoint xq."""
-    dx_fp32 = _fp32(dX)
-    _check(_lib.sbl_b8_linear_backward(wd, _b8ref(w_t), _b8ref(xq), x_type, _of(dY, _BF16), _ld(dY), T, g_type,
-                                       _flat(dX, _F32 if dx_fp32 else _BF16), dx_fp32, _flat(dW, _F32), 1 if accumulate else 0,
-                                       *_space(workspace), _here(w_t and w_t.codes, xq and xq.codes, dY, dX, dW, workspace)),
-           "sbl_b8_linear_backward")
+    dev, dx = _device(), _float(dX)
+    _check(_lib.sbl_b8_linear_backward(wd, _b8ref(w_t, dev), _b8ref(xq, dev), x_type, _rows(dY, _BF16, dev), _ld(dY), T, g_type,
+                                       _flat(dX, dx, dev), 1 if dx is _F32 else 0, _flat(dW, _F32, dev), 1 if accumulate else 0,
+                                       _flat(workspace, None, dev), 0 if workspace is None else workspace.nbytes,
+                                       _stream_of(dev)), "sbl_b8_linear_backward")
 
 
 def sbl_glu_forward(d: sbl_b8_desc, act: int, G: torch.Tensor, U: Optional[torch.Tensor], H: Optional[torch.Tensor],
                     g8: Optional[Block8] = None, u8: Optional[Block8] = None) -> None:
     """H = act(G) * U and the checkpoints of G and U; every output optional."""
-    _check(_lib.sbl_glu_forward(d, act, _of(G, _BF16), _ld(G), _of(U, _BF16), _ld(U), _of(H, _BF16), _ld(H), _b8ref(g8),
-                                _b8ref(u8), _here(G, U, H, g8 and g8.codes, u8 and u8.codes)), "sbl_glu_forward")
+    dev = _device()
+    _check(_lib.sbl_glu_forward(d, act, _rows(G, _BF16, dev), _ld(G), _rows(U, _BF16, dev), _ld(U), _rows(H, _BF16, dev), _ld(H),
+                                _b8ref(g8, dev), _b8ref(u8, dev), _stream_of(dev)), "sbl_glu_forward")
 
 
 def sbl_glu_backward(d: sbl_b8_desc, act: int, g8: Block8, u8: Optional[Block8], dH: torch.Tensor, dG: torch.Tensor,
                      dU: Optional[torch.Tensor]) -> None:
-    _check(_lib.sbl_glu_backward(d, act, _b8ref(g8), _b8ref(u8), _of(dH, _BF16), _ld(dH), _of(dG, _BF16), _ld(dG),
-                                 _of(dU, _BF16), _ld(dU), _here(g8 and g8.codes, u8 and u8.codes, dH, dG, dU)), "sbl_glu_backward")
+    dev = _device()
+    _check(_lib.sbl_glu_backward(d, act, _b8ref(g8, dev), _b8ref(u8, dev), _rows(dH, _BF16, dev), _ld(dH), _rows(dG, _BF16, dev),
+                                 _ld(dG), _rows(dU, _BF16, dev), _ld(dU), _stream_of(dev)), "sbl_glu_backward")
 
 
 def sbl_quantize_act_rmsnorm_checkpoint(d: sbl_b8_desc, X: torch.Tensor, g: Optional[torch.Tensor], eps: float,
                                         Xq: torch.Tensor, dscale: torch.Tensor, x8: Block8) -> None:
-    _check(_lib.sbl_quantize_act_rmsnorm_checkpoint(d, _flat(X, _BF16), _flat(g, _BF16), float(eps), _flat(Xq, _I8), _flat(dscale, _F32),
-                                                    _b8ref(x8), _here(X, g, Xq, dscale, x8 and x8.codes)), "sbl_quantize_act_rmsnorm_checkpoint")
+    dev = _device()
+    _check(_lib.sbl_quantize_act_rmsnorm_checkpoint(d, _flat(X, _BF16, dev), _flat(g, _BF16, dev), float(eps), _flat(Xq, _I8, dev),
+                                                    _flat(dscale, _F32, dev), _b8ref(x8, dev), _stream_of(dev)),
+           "sbl_quantize_act_rmsnorm_checkpoint")
 
 
 def sbl_rmsnorm_backward_workspace_bytes(T: int, K: int) -> int:
@@ -584,8 +582,10 @@ def sbl_rmsnorm_backward(d: sbl_b8_desc, x8: Block8, g: Optional[torch.Tensor], 
                          dR: Optional[torch.Tensor], dX: torch.Tensor, dg: Optional[torch.Tensor],
                          workspace: Optional[torch.Tensor]) -> None:
     """dX (+ dR) and the gains' gradient dg from the checkpointed norm input x8."""
-    _check(_lib.sbl_rmsnorm_backward(d, _b8ref(x8), _flat(g, _BF16), float(eps), _flat(dU, _BF16), _flat(dR, _BF16), _flat(dX, _BF16),
-                                     _flat(dg, _F32), *_space(workspace), _here(x8 and x8.codes, g, dU, dR, dX, dg, workspace)), "sbl_rmsnorm_backward")
+    dev = _device()
+    _check(_lib.sbl_rmsnorm_backward(d, _b8ref(x8, dev), _flat(g, _BF16, dev), float(eps), _flat(dU, _BF16, dev), _flat(dR, _BF16, dev),
+                                     _flat(dX, _BF16, dev), _flat(dg, _F32, dev), _flat(workspace, None, dev),
+                                     0 if workspace is None else workspace.nbytes, _stream_of(dev)), "sbl_rmsnorm_backward")
 
 
 # ------------------------------------------------- allocation helpers (torch)

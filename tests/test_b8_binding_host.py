@@ -1,6 +1,8 @@
 """What the Python binding of the 8-bit block operators refuses before the library sees a pointer: tensors that the
 C arguments cannot describe.  No device is needed, and none may be present: a call let through would hand host
 pointers to kernels."""
+import sys
+
 import pytest
 import torch
 
@@ -16,6 +18,13 @@ def sbl():
     if torch.cuda.is_available():
         pytest.skip("a device is present: host pointers must not reach kernels")
     return m
+
+
+@pytest.fixture
+def placed(sbl, monkeypatch):
+    """The host's tensors pass for tensors of device 0, the current one."""
+    monkeypatch.setattr(sbl, "_device", lambda: 0)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
 
 
 def z(*shape, dtype=BF):
@@ -52,7 +61,7 @@ ARGUMENTS = [(c, a) for c, names in (
 
 
 @pytest.mark.parametrize("call,name", ARGUMENTS)
-def test_other_element_types_are_refused(sbl, call, name):
+def test_other_element_types_are_refused(sbl, placed, call, name):
     f, args = calls(sbl)[call]
     right = {BF, F32} if (call, name) in EITHER else {args[name].dtype}
     for dtype in (torch.float16, torch.float64, torch.int16, torch.uint8, BF, F32, I8):
@@ -67,7 +76,7 @@ STRIDED = {("quantize", "X"), ("dequantize", "X"), ("gemm", "D"), ("linear_forwa
 
 
 @pytest.mark.parametrize("call,name", [x for x in ARGUMENTS if x not in STRIDED])
-def test_slices_of_wider_buffers_are_refused_where_there_is_no_stride(sbl, call, name):
+def test_slices_of_wider_buffers_are_refused_where_there_is_no_stride(sbl, placed, call, name):
     f, args = calls(sbl)[call]
     t = args[name]
     wide = torch.zeros(*t.shape[:-1], 2 * t.shape[-1], dtype=t.dtype)
@@ -79,14 +88,14 @@ def test_slices_of_wider_buffers_are_refused_where_there_is_no_stride(sbl, call,
 
 
 @pytest.mark.parametrize("call,name", sorted(STRIDED))
-def test_rows_themselves_have_to_be_contiguous(sbl, call, name):
+def test_rows_themselves_have_to_be_contiguous(sbl, placed, call, name):
     f, args = calls(sbl)[call]
     t = args[name]
     with pytest.raises(ValueError, match="contiguous rows"):
         f(**{**args, name: torch.zeros(t.shape[0], 2 * t.shape[1], dtype=t.dtype)[:, ::2]})
 
 
-def test_workspaces_and_stored_matrices_are_contiguous(sbl):
+def test_workspaces_and_stored_matrices_are_contiguous(sbl, placed):
     d, wd = sbl.b8_desc(T, K), sbl.b8_desc(O, K)
     m = sbl.alloc_b8(d, device="cpu")
     gaps = torch.zeros(1 << 21, dtype=torch.uint8)[::2]
@@ -99,22 +108,34 @@ def test_workspaces_and_stored_matrices_are_contiguous(sbl):
             sbl.Block8(codes=codes, scales=scales)
 
 
-@pytest.mark.parametrize("missing", ["_raw_device", "_raw_stream"])
+@pytest.mark.parametrize("missing", ["_cuda_getDevice", "_cuda_getCurrentRawStream"])
 def test_stream_without_torchs_private_names(sbl, monkeypatch, missing):
+    """The binding loaded again where torch lacks one of them."""
+    import importlib.util
+
     class Stream:
         cuda_stream = 0x5EED
 
-    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
-    monkeypatch.setattr(sbl, "_raw_device", lambda: 3)
-    monkeypatch.setattr(sbl, "_raw_stream", lambda d: 0x1000 + d)
-    assert sbl._stream() == 0x1003
-    monkeypatch.setattr(sbl, missing, None)
-    assert sbl._stream() == 0x5EED
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: Stream if dev == 3 else None)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 3, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0x1000 + dev, raising=False)
+
+    def load():
+        spec = importlib.util.spec_from_file_location("sbl_again", sbl.__file__)
+        m = importlib.util.module_from_spec(spec)
+        monkeypatch.setitem(sys.modules, "sbl_again", m)
+        spec.loader.exec_module(m)
+        return m
+
+    assert load()._stream() == 0x1003
+    monkeypatch.delattr(torch._C, missing)
+    assert load()._stream() == (0x1003 if missing == "_cuda_getDevice" else 0x5EED)
 
 
 @pytest.mark.parametrize("call", sorted({c for c, _ in ARGUMENTS}))
-def test_host_tensors_are_refused(sbl, call):
+def test_host_tensors_are_refused(sbl, call, monkeypatch):
+    monkeypatch.setattr(sbl, "_device", lambda: 0)
     f, args = calls(sbl)[call]
     with pytest.raises(ValueError, match="device"):
         f(**args)
@@ -132,9 +153,8 @@ def test_tensors_of_another_device_are_refused(sbl, call, name, monkeypatch):
     def stream(device):
         raise Reached
 
-    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
-    monkeypatch.setattr(sbl, "_raw_device", lambda: 0)
-    monkeypatch.setattr(sbl, "_raw_stream", stream)
+    monkeypatch.setattr(sbl, "_device", lambda: 0)
+    monkeypatch.setattr(sbl, "_stream_of", stream)
     monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 1 if self is odd else 0)
     with pytest.raises(ValueError, match="a tensor of device 1"):
         f(**args)
@@ -148,8 +168,7 @@ def test_stored_matrices_of_another_device_are_refused(sbl, monkeypatch):
     m, w, wt = (sbl.alloc_b8(x, device="cpu") for x in (d, wd, sbl.b8_desc(K, O)))
     with pytest.raises(ValueError, match="one device"):
         sbl.Block8(codes=m.codes, scales=m.scales.to("meta"))
-    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
-    monkeypatch.setattr(sbl, "_raw_device", lambda: 0)
+    monkeypatch.setattr(sbl, "_device", lambda: 0)
     for odd in (m, w, wt):
         monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 1 if self is odd.codes else 0)
         with pytest.raises(ValueError, match="a tensor of device 1"):
