@@ -59,6 +59,15 @@ static sbl_status b8_device(HostDevice *hd)
     return SBL_OK;
 }
 
+// The status of a launch or a memset.  A failed one (a stream whose capture was broken, say)
+// leaves no error behind: it would be taken for the next call's.
+static sbl_status launched(cudaError_t e)
+{
+    if (e == cudaSuccess) return SBL_OK;
+    cudaGetLastError();
+    return SBL_ERR_CUDA;
+}
+
 // Launch with programmatic dependent launch: a kernel waits for the one before
 // it (griddepcontrol.wait) before it touches global memory, or, one that neither
 // reads nor writes what the one before it writes (`late`), before it ends.
@@ -77,8 +86,7 @@ static sbl_status launch2(void (*kernel)(P...), int64_t grid, int64_t grid_y, in
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return SBL_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? SBL_OK : SBL_ERR_CUDA;
+    return launched(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 template <typename... P, typename... A>
@@ -105,8 +113,7 @@ static sbl_status launch_cluster(void (*kernel)(P...), int64_t grid, int cluster
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return SBL_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? SBL_OK : SBL_ERR_CUDA;
+    return launched(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 // Scale words (512 columns) a warp of the element-wise kernels takes: one
@@ -316,8 +323,7 @@ static sbl_status launch_b8_gemm(const HostDevice &hd, const sbl_b8_desc *ad, co
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, b8_gemm_kernel<BN, LONG>, ta, tb, tsa, tsb, ty, args) != cudaSuccess) return SBL_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? SBL_OK : SBL_ERR_CUDA;
+    return launched(cudaLaunchKernelEx(&cfg, b8_gemm_kernel<BN, LONG>, ta, tb, tsa, tsb, ty, args));
 }
 
 // How the product of few tokens runs: padded tokens, CTAs that share K, stages.
@@ -373,8 +379,7 @@ static sbl_status launch_skinny_nt(const HostDevice &hd, const SkinnyPlan &p, co
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.split > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, b8_skinny_kernel<TYPE, NT, FUSED>, tw, tx, a) != cudaSuccess) return SBL_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? SBL_OK : SBL_ERR_CUDA;
+    return launched(cudaLaunchKernelEx(&cfg, b8_skinny_kernel<TYPE, NT, FUSED>, tw, tx, a));
 }
 
 // Y [T, O] = X W^T for few tokens.  X: bf16 (quantised in the kernel, xq an
@@ -748,8 +753,7 @@ sbl_status sbl_b8_linear_backward(const sbl_b8_desc *w_desc, const sbl_b8 *w_t, 
     if ((st = b8_device(&hd)) != SBL_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) {
-        if (dW && !dw_accumulate && cudaMemsetAsync(dW, 0, static_cast<size_t>(O) * K * 4, s) != cudaSuccess) return SBL_ERR_CUDA;
-        return SBL_OK;
+        return dW && !dw_accumulate ? launched(cudaMemsetAsync(dW, 0, static_cast<size_t>(O) * K * 4, s)) : SBL_OK;
     }
     const BackwardPlan p = backward_plan(O, K, T, g_type, x_type);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -898,8 +902,7 @@ sbl_status sbl_rmsnorm_backward(const sbl_b8_desc *desc, const sbl_b8 *x8, const
     if ((st = b8_device(&hd)) != SBL_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) {
-        if (dg && cudaMemsetAsync(dg, 0, static_cast<size_t>(K) * 4, s) != cudaSuccess) return SBL_ERR_CUDA;
-        return SBL_OK;
+        return dg ? launched(cudaMemsetAsync(dg, 0, static_cast<size_t>(K) * 4, s)) : SBL_OK;
     }
     NormBwdArgs a;
     memset(&a, 0, sizeof(a));

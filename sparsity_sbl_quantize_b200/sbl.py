@@ -569,7 +569,7 @@ def sbl_glu_backward(d: sbl_b8_desc, act: int, g8: Block8, u8: Optional[Block8],
 def sbl_quantize_act_rmsnorm_checkpoint(d: sbl_b8_desc, X: torch.Tensor, g: Optional[torch.Tensor], eps: float,
                                         Xq: torch.Tensor, dscale: torch.Tensor, x8: Block8) -> None:
     dev = _device()
-    _check(_lib.sbl_quantize_act_rmsnorm_checkpoint(d, _flat(X, _BF16, dev), _flat(g, _BF16, dev), float(eps), _flat(Xq, _I8, dev),
+    _check(_lib.sbl_quantize_act_rmsnorm_checkpoint(d, _flat(X, _BF16, dev), _flat(g, _BF16, dev), eps, _flat(Xq, _I8, dev),
                                                     _flat(dscale, _F32, dev), _b8ref(x8, dev), _stream_of(dev)),
            "sbl_quantize_act_rmsnorm_checkpoint")
 
@@ -583,7 +583,7 @@ def sbl_rmsnorm_backward(d: sbl_b8_desc, x8: Block8, g: Optional[torch.Tensor], 
                          workspace: Optional[torch.Tensor]) -> None:
     """dX (+ dR) and the gains' gradient dg from the checkpointed norm input x8."""
     dev = _device()
-    _check(_lib.sbl_rmsnorm_backward(d, _b8ref(x8, dev), _flat(g, _BF16, dev), float(eps), _flat(dU, _BF16, dev), _flat(dR, _BF16, dev),
+    _check(_lib.sbl_rmsnorm_backward(d, _b8ref(x8, dev), _flat(g, _BF16, dev), eps, _flat(dU, _BF16, dev), _flat(dR, _BF16, dev),
                                      _flat(dX, _BF16, dev), _flat(dg, _F32, dev), _flat(workspace, None, dev),
                                      0 if workspace is None else workspace.nbytes, _stream_of(dev)), "sbl_rmsnorm_backward")
 
