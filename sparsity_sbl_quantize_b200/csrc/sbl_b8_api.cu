@@ -449,7 +449,7 @@ static sbl_status gemm(const HostDevice &hd, const sbl_b8_desc *ad, const sbl_b8
     args.out_fp32 = fp32 ? 1 : 0;
     args.accumulate = accumulate ? 1 : 0;
     // Few rows: the kernel that splits K.  It measured faster up to 64 rows
-    // (6912 x 2560 at 64: 9.1 us against 11.0; 2560 x 6912: 9.5 against 23.5),
+    // (n x k: 6912 x 2560 at 64: 9.1 us against 11.0; 2560 x 6912: 9.5 against 23.5),
     // and to 128 only where the other's tiles leave most SMs idle (2560 x 6912 at
     // 128: 11.6 against 23.8; 11008 x 2048: 13.4 against 10.4).
     const int64_t tiles_w = (args.N + kBM - 1) / kBM;
@@ -462,7 +462,7 @@ static sbl_status gemm(const HostDevice &hd, const sbl_b8_desc *ad, const sbl_b8
     // 128 x 256 tiles or 128 x 128 ones, of which a product with few tiles has
     // twice as many: the time of a launch in units of 10 ns fits
     // 460 + rounds (42 blocks + 60) and 340 + rounds (34 blocks + 45)
-    // (16384 x 2048 x 11008: 269 against 440 us; 512 x 6912 x 2560: 14.0 against 18.3;
+    // (m x n x k: 16384 x 2048 x 11008: 269 against 440 us; 512 x 6912 x 2560: 14.0 against 18.3;
     // 300 x 4864 x 896: 6.6 against 5.9; 777 x 1536 x 1536: 8.5 against 8.0).
     auto rounds = [&](int64_t bn) {
         return ((static_cast<int64_t>(args.M) + kBM - 1) / kBM * ((args.N + bn - 1) / bn) + hd.num_sms - 1) / hd.num_sms;
@@ -712,7 +712,7 @@ sbl_status sbl_b8_linear_forward(const sbl_b8_desc *w_desc, const sbl_b8 *w, con
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // One launch that quantises X itself while each CTA's share of it is
     // small, up to 112 (token, block) pairs; 120 measured even with two launches
-    // (6912 x 2560: 1 token, 5 pairs, 7.3 us against 9.1, 16 tokens, 80 pairs, 8.5
+    // (n x k: 6912 x 2560: 1 token, 5 pairs, 7.3 us against 9.1, 16 tokens, 80 pairs, 8.5
     // against 9.8, 24 tokens, 120 pairs, 10.4 against 10.2; 2560 x 6912: 16 tokens,
     // 112 pairs, 9.6 against 10.6).
     if (T <= 64) {

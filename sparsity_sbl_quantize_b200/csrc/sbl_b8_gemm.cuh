@@ -16,15 +16,17 @@
 // Tiles are 128 x BN (256, or 128 where that spreads a small product over more
 // SMs); roles as in the other tcgen05 products: warp 0 TMA loads, warp 1 MMAs,
 // warps 2-9 the epilogue.  CTA pairs with 256 x 256 tiles were built first and
-// gave way to this (16384 x 11008 x 2048: 309 us against 299, 16384 x 2048 x 11008:
-// 296 against 269).  That was no comparison on equal terms: the pair kernel issued
+// gave way to this (m x n x k, here and below: 16384 x 11008 x 2048: 309 us against
+// 299, 16384 x 2048 x 11008: 296 against 269).  That was no comparison on equal terms: the pair kernel issued
 // from a lane-0 branch and copied scales one word at a time, which cost the
 // single-CTA kernel 5% and more (below).  Pairs with an elected lane and two-word
 // copies have not been measured.
 //
-// 16384 x 2048 x 11008 takes 269 us, 2.7 PFLOP/s (twice the measured sustained
-// bf16 rate); the same MMAs without loads or scales take 232: the rest is the
-// tensor core waiting between stages and tiles.
+// 16384 x 2048 x 11008 takes 269 us in short runs, 2.7 PFLOP/s (84% of twice the
+// measured burst bf16 rate, cuBLAS's); the same MMAs without loads or scales take
+// 232: the rest is the tensor core waiting between stages and tiles (active 67% of
+// the cycles at 8192 x 11008 x 2048).  In a loop of seconds the power limit takes
+// another 12%, as it takes 14% of cuBLAS's bf16 product.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -198,9 +198,10 @@ __global__ void __launch_bounds__(256) glu_backward_kernel(GluBwdArgs a)
 // registers; the parts meet in shared memory (rows of one CTA, in order) and
 // then in norm_dgain_kernel (CTAs, in order), so the result is the same every
 // time.
-// 16384 x 2048 with the residual gradient: 44 us, 5.3 TB/s (one row's latency, its
-// barrier and 128 registers a thread bound it, not DRAM); rows over 8192, with a
-// cluster barrier a row, 2.9 TB/s.
+// 16384 x 2048 with the residual gradient: 45 us, 5.2 TB/s: two CTAs an SM (128
+// registers a thread) issue 2.6 of 4 instructions a clock while each waits out a
+// row's latency and barrier, at 62% of DRAM's rate.  Rows over 8192, with a
+// cluster barrier a row: 2.4 TB/s (4096 x 11008).
 constexpr int kNormPartials = 640;  // most partial rows of dgain
 constexpr int kNormLongThreads = 512;
 constexpr int kNormMaxSplit = 8;    // CTAs a row: 8 x 512 chunks of 16 = 65536
