@@ -650,7 +650,7 @@ sbl_status sbl_quantize_act_rmsnorm_checkpoint(const sbl_b8_desc *desc, const ui
  * dU, dR, dX: bf16 [T, K] contiguous; dg: fp32 [K], the same bits for the
  * same inputs on the same kind of device.  fp32 arithmetic on n = x r and
  * dX = r (dU g - n mean(dU g n)), sums scaled by the row's largest block exponent:
- * neither x^2 nor r^3 has to lie in fp32's range.  r is at most 2^126: a smaller
+ * neither x^2 nor r^3 has to lie in fp32's range (|dU g| up to 2^96).  r is at most 2^126: a smaller
  * mean x^2 + eps than 2^-252 (rows of zeros with eps 0) counts as 2^-252.  A row
  * with a marked block gives NaN in its dX and in dg.  The quantiser's gradient is the
  * straight-through one of the summary pages (dU = the linear's dX).

@@ -53,7 +53,10 @@ static sbl_status b8_device(HostDevice *hd)
         allow(b8_skinny_kernel<0, 32, false>);
         allow(b8_skinny_kernel<0, 64, false>);
         allow(b8_skinny_kernel<0, 128, false>);
-        if (st2 != SBL_OK) return st2;
+        if (st2 != SBL_OK) {
+            cudaGetLastError();
+            return st2;
+        }
         g_b8_ready[hd->index] = true;
     }
     return SBL_OK;

@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(RT > 256 ? RT : 256, RT > 256 ? 1 : 2) norm_ba
         }
         if constexpr (RT == kNormLongThreads) {
             if (a.split > 1) {
-                // each CTA's sums to all of the cluster, then added in rank
-                // order; again two buffers and one barrier
+                // each CTA's sums to all of the cluster, joined in every CTA
+                // alike; again two buffers and one barrier
                 if (lt < a.split) {
                     const uint32_t to = map_shared_rank(smem_addr(&parts[parity][rank]), lt);
                     asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to), "f"(s.s1) : "memory");
